@@ -52,7 +52,8 @@ typedef enum {
     EVA_ERR_DEVICE_TIMEOUT = 5,  /* a bounded device wait gave up                */
     EVA_ERR_NO_DEVICE = 6,       /* no sm_100 device is current                  */
     EVA_ERR_DEVICE_CHECK = 7,    /* checked build: a kernel access was out of bounds */
-    EVA_ERR_SCRATCH_TOO_SMALL = 8 /* eva_vq_linear_run_noalloc: B * K * 4 > 4 MiB      */
+    EVA_ERR_SCRATCH_TOO_SMALL = 8, /* eva_vq_linear_run_noalloc: B * K * 4 > 4 MiB     */
+    EVA_ERR_BAD_INDEX = 9        /* a row start, length or page on the device was out of range */
 } eva_status_t;
 
 typedef enum { EVA_F16 = 0, EVA_F32 = 1 } eva_dtype_t;
@@ -383,6 +384,175 @@ EVA_API eva_status_t eva_vq_kmeans_update(const float *v, int64_t M, int32_t d, 
 EVA_API eva_status_t eva_vq_residual(const float *wrot, int32_t N, int32_t K, const void *wc, int32_t ncent,
                                      const uint8_t *wi, int32_t codebook_rows, int32_t group,
                                      uint8_t *signs_out, void *alpha_out, eva_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Between a block's q, k, v layers and its o layer: rotary positions (with
+ * the heads' norms), the 8-bit cache of keys and values, and attention over
+ * it.  No counterpart in the pages, which describe the linear layers only:
+ * these take the rows that q, k and v write and give the rows that o reads.
+ * All calls are asynchronous on `stream` and allocate nothing; a handle's
+ * device is made current for the call.  Arrays named below as device int32
+ * are read on the device, so a captured call follows their contents.
+ * ---------------------------------------------------------------------- */
+
+/* Which dimensions of a head turn together: i and i + R/2, or 2i and 2i + 1. */
+typedef enum { EVA_ROPE_HALF = 0, EVA_ROPE_INTERLEAVED = 1 } eva_rope_layout_t;
+
+/*
+ * Frequencies f_i = theta^(-2i/R), i < R/2 = rotary_dim / 2, and how they
+ * are scaled for contexts longer than the model's own:
+ *   LINEAR  f / factor
+ *   NTK     theta * factor^(R / (R - 2)) in place of theta
+ *   YARN    f (1 - r) + f / factor r, r = clamp((i - a) / (b - a), 0, 1) with
+ *           a = max(floor(e(high)), 0), b = min(ceil(e(low)), R - 1) (b - a at least 0.001),
+ *           e(n) = R ln(original / (2 pi n)) / (2 ln theta): pairs that turn
+ *           more than `high` times over `original` tokens keep f, those below
+ *           `low` times get f / factor; cos and sin times 0.1 ln(factor) + 1
+ *   BANDS   the same blend linear in the turns n = original f / (2 pi):
+ *           f / factor (1 - s) + f s, s = clamp((n - low) / (high - low), 0, 1)
+ */
+typedef enum {
+    EVA_ROPE_UNSCALED = 0, EVA_ROPE_LINEAR = 1, EVA_ROPE_NTK = 2, EVA_ROPE_YARN = 3, EVA_ROPE_BANDS = 4
+} eva_rope_scaling_t;
+
+typedef struct {
+    int32_t q_heads, kv_heads;  /* heads of q and of k; either may be 0 (not both)        */
+    int32_t head_dim;           /* 1..1024                                                */
+    int32_t rotary_dim;         /* R: even, 0..head_dim; the other dimensions pass through */
+    int32_t layout;             /* eva_rope_layout_t                                      */
+    int32_t norm;               /* 1: RMS norm of each head first                         */
+    eva_dtype_t in_dtype, out_dtype;
+    int32_t scaling;            /* eva_rope_scaling_t                                     */
+    float eps;                  /* of the norm                                            */
+    float weight_offset;        /* the norm multiplies by weight + weight_offset          */
+    double theta;
+    double factor, original, low, high;   /* of the scaling; ignored where it has no use  */
+    double magnitude;           /* > 0: multiplies cos and sin in place of the scaling's own */
+} eva_rope_desc;
+
+typedef struct eva_rope *eva_rope_t;
+
+/* q_weight, k_weight: device fp16 [head_dim] (copied), or NULL for a norm without
+ * weights; both NULL without a norm.  Waits for `stream`. */
+EVA_API eva_status_t eva_rope_create(eva_rope_t *out, const eva_rope_desc *desc, const void *q_weight,
+                                     const void *k_weight, eva_stream_t stream);
+
+/*
+ * Norm and turn T tokens' heads in one pass.  q: [T][q_heads][head_dim], ldq
+ * elements from one token to the next (at least q_heads * head_dim, so q may be
+ * a column range of a fused projection's rows); k, q_out, k_out likewise.
+ * positions: device int32 [T], any value (NULL when rotary_dim is 0).  Angles are
+ * exact to the fp32 rounding of the reduced angle at every position.  The
+ * input types' arithmetic is fp32, rounded once.  q_out may be q (k_out k) when
+ * the types and strides are equal; otherwise outputs must not overlap inputs.
+ * Any alignment of the element type works; 16-byte aligned rows with head_dim
+ * and rotary_dim multiples of 16 are faster.
+ */
+EVA_API eva_status_t eva_rope_run(eva_rope_t h, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                                  const int32_t *positions, int32_t T, void *q_out, int64_t ldqo, void *k_out,
+                                  int64_t ldko, eva_stream_t stream);
+EVA_API eva_status_t eva_rope_destroy(eva_rope_t h);
+
+/* How the cache holds a value x = scale * code: code an int8 in [-127, 127]
+ * with scale = max |x| / 127, or an e4m3 float with scale = max |x| / 448. */
+typedef enum { EVA_CACHE_INT8 = 0, EVA_CACHE_E4M3 = 1 } eva_cache_dtype_t;
+
+typedef struct {
+    int32_t q_heads, kv_heads;  /* q_heads a multiple of kv_heads                         */
+    int32_t head_dim;           /* 64, 128 or 256                                         */
+    int32_t page_size;          /* tokens a page: 16, 32, 64, 128 or 256                  */
+    int32_t num_pages;          /* pages of the buffers                                   */
+    int32_t max_seqs;           /* largest B of a call                                    */
+    int32_t max_pages;          /* columns of the page tables                             */
+    int32_t cache_dtype;        /* eva_cache_dtype_t                                      */
+    eva_dtype_t out_dtype;      /* of the attention output                                */
+    int32_t window;             /* 0: every earlier key; w: the last w keys, itself included */
+    float softcap;              /* 0: none; c: scores become c tanh(score / c)            */
+    float scale;                /* of the scores; 0: 1 / sqrt(head_dim)                   */
+} eva_kv_desc;
+
+typedef struct eva_kv *eva_kv_t;
+
+/*
+ * A cache over caller-owned device buffers (16-byte aligned):
+ *   k_pages, v_pages  codes [num_pages][kv_heads][page_size][head_dim], one byte each
+ *   k_scale, v_scale  fp32 [num_pages][kv_heads]
+ * They keep their contents and must live as long as the handle.  The handle owns
+ * the workspace of eva_kv_attend.  Waits for `stream`.
+ */
+EVA_API eva_status_t eva_kv_create(eva_kv_t *out, const eva_kv_desc *desc, void *k_pages, void *v_pages, float *k_scale,
+                                   float *v_scale, eva_stream_t stream);
+
+/*
+ * Common to the next three calls: T packed rows of B sequences, 1 <= B <= max_seqs.
+ *   starts      device int32 [B + 1]: sequence b has rows starts[b] .. starts[b+1] - 1
+ *               (non-decreasing, at most T); rows behind starts[B] are neither
+ *               read nor written, so a padded batch may leave some
+ *   lens        device int32 [B]: each sequence's length WITH those rows: row i
+ *               of n is at position lens[b] - n + i
+ *   page_table  device int32 [B][max_pages]: page of positions
+ *               [j page_size, (j + 1) page_size) of sequence b at [b][j]; entries
+ *               behind its length are not read
+ * A length or row range that cannot be right drops its sequence, a page outside
+ * [0, num_pages) drops its tokens (they count as masked), and eva_kv_sync_status then returns
+ * EVA_ERR_BAD_INDEX.
+ */
+
+/*
+ * Write the keys and values of T new tokens: k and v [T][kv_heads][head_dim] of in_dtype,
+ * ldk and ldv elements from one token to the next (rows 16-byte aligned).
+ * Writing slot 0 of a page gives it a new scale; writing behind kept tokens
+ * takes the larger of the page's scale and the new tokens', and where it grows
+ * the kept codes are rounded again in its units.  Values beyond +-65504 are
+ * stored as +-65504 and a NaN as 0.  Rows at negative positions (a length below the row
+ * count) are not written.  A page that is written must belong to one sequence of
+ * the call: two that share one race on it.
+ */
+EVA_API eva_status_t eva_kv_append(eva_kv_t h, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                   eva_dtype_t in_dtype, const int32_t *starts, const int32_t *lens,
+                                   const int32_t *page_table, int32_t B, int32_t T, eva_stream_t stream);
+
+/*
+ * The stored values back: rows starts[b] .. of k_out and v_out ([T][kv_heads][head_dim] of out_dtype,
+ * contiguous; either may be NULL) are the tokens at positions begins[b] ..
+ * of sequence b.
+ */
+EVA_API eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_t *begins, const int32_t *page_table,
+                                 int32_t B, int32_t T, eva_dtype_t out_dtype, void *k_out, void *v_out,
+                                 eva_stream_t stream);
+
+/*
+ * Causal attention of T rows over the cache: q fp16 [T][q_heads][head_dim] (ldq elements from one token
+ * to the next, rows 16-byte aligned); out [T][q_heads][head_dim] of the descriptor's out_dtype,
+ * contiguous; lse (optional) fp32 [T][q_heads], the natural logarithm of the sum of
+ * exponentials.  The row at position p sees keys j <= p, with a window j > p - window.  A row that
+ * sees no key gives zeros and lse = -infinity.  Statistics and sums are fp32; the
+ * softmax weights are rounded to fp16 for the value product.  Results do not depend
+ * on timing; they may differ in the last bits between batches, whose work is
+ * cut at other places.  The handle's workspace is shared: one handle must not attend on two
+ * streams at once, captured graphs included (give each stream a handle over the same buffers).
+ */
+EVA_API eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t *starts, const int32_t *lens,
+                                   const int32_t *page_table, int32_t B, int32_t T, void *out, float *lse,
+                                   eva_stream_t stream);
+
+/* Synchronises the device, reports and clears the handle's error word:
+ * EVA_ERR_BAD_INDEX (above) or EVA_ERR_DEVICE_TIMEOUT (a bounded wait gave up; that
+ * call's outputs are undefined). */
+EVA_API eva_status_t eva_kv_sync_status(eva_kv_t h);
+
+/* Failure-detection test hook: the next eva_kv_attend streams nothing, so that its waits
+ * run out after `rounds` tries (1 .. 2^20).  One-shot; its outputs are undefined. */
+EVA_API eva_status_t eva_kv_debug_inject_wait_timeout(eva_kv_t h, int32_t rounds);
+
+typedef struct {
+    int64_t workspace_bytes;
+    int32_t sm_count;
+    int32_t rows, grid, stages; /* last attention call: rows an item, CTAs, steps of 32 tokens in flight a CTA */
+} eva_kv_info;
+EVA_API eva_status_t eva_kv_cache_info(eva_kv_t h, eva_kv_info *info);
+
+EVA_API eva_status_t eva_kv_destroy(eva_kv_t h);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,673 @@
+// eva_attend.cuh -- attention of new tokens over the paged 8-bit cache.
+//
+// For every row (token, query head) at position p of its sequence
+//   z_j = scale * q.k_j,  optionally cap * tanh(z_j / cap),  j <= p, j > p - window
+//   o = sum_j e^(z_j - m) v_j / sum_j e^(z_j - m)
+// in one pass over the cache with the running maximum m and sum.  k_j = sk c_j
+// and v_j = sv d_j with 8-bit codes and one scale a page and head.
+//
+// What bounds it: a decode step reads each cached byte once for a handful of
+// multiplications, so bytes; everything else has to fit beside the stream.
+//  - Codes become f16 exactly (int8: a byte under exponent 2^10, minus 1152;
+//    e4m3: sign and magnitude shifted into an f16's fields, times 2^8) and go
+//    to the tensor cores as the A operand: 16 tokens x 16 dimensions of keys,
+//    16 dimensions x 16 tokens of values.  Rows are the MMA's N (8 at a time),
+//    so a decode step of one to eight queries a key head wastes nothing, and
+//    more rows reuse the converted codes.  Warp-level MMAs: at eight rows the
+//    product is 2 % of the tensor rate at full stream speed; the conversion
+//    into registers is the work, and tcgen05 would take it through tensor
+//    memory first.
+//  - Scales never touch the codes: sk multiplies the finished score, sv enters
+//    the exponent.  With w_j = e^(z_j - M) sv and M the running maximum of
+//    z_j + ln sv, the weights stay in (0, 1] whatever the pages' scales are;
+//    the sum of the softmax gets w_j / sv.  w_j is rounded to f16 (one
+//    2^-12 error a weight, averaged over the keys); all sums and statistics are
+//    fp32.
+//  - One warp streams: it looks pages up, and copies 32 tokens of keys and
+//    values a step into a ring of shared memory (TMA, 128-byte swizzle: both
+//    ldmatrix patterns are free of bank conflicts).  A page id outside the
+//    cache is never used as an address: its tokens count as masked and the
+//    status word is set.
+//  - Work is cut on the device, because only the device knows the lengths: the
+//    steps of all (sequence, row tile, key head) items form one line, and each
+//    CTA takes an equal part of it, whatever the items' borders.  An item that
+//    several CTAs share is joined by the last of them to finish, in the order
+//    of the parts, so results do not depend on timing.
+#pragma once
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "eva_kv.cuh"
+
+namespace eva {
+
+constexpr int kAtStep = 32;            // tokens a step
+constexpr int kAtStatusWait = 1;       // status bit: a bounded wait gave up
+
+struct AttendParams {
+    KvTokens tok;
+    const __half *q;                   // [T][Hq][D], ldq elements a token
+    long long ldq;
+    const float *k_scale, *v_scale;    // [pages][H]
+    void *out;                         // [T][Hq][D]
+    float *lse;                        // [T][Hq] or null
+    float *part;                       // [2 grid][rows][D] unnormalised outputs of shared items
+    float2 *part_ml;                   // [2 grid][rows] maximum (base 2) and sum
+    int *counters;                     // [grid], zero between calls
+    int *status;
+    int Hq, H, G;                      // query heads, key heads, queries a key head
+    int window, out_f32, min_steps, wait_rounds;
+    int inject;                        // test hook: stream nothing, so that every wait runs out
+    float scale, cap;                  // cap 0: none
+};
+
+struct alignas(64) AttendMaps {
+    CUtensorMap k, v;                  // codes as rows of D bytes: [pages * H * page][D]
+};
+
+// ---------------------------------------------------------------- small PTX
+
+__device__ __forceinline__ void at_tma_2d(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void at_ldsm(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void at_ldsm_t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t at_transpose(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void at_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float at_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four codes -> two pairs of f16: neighbours (b0 b1, b2 b3: dimensions of a
+// key) or every other (b0 b2, b1 b3: a dimension of two tokens' values).
+template <bool E4M3>
+struct AtCode;
+template <>
+struct AtCode<false> {
+    static constexpr float kUnit = 1.f;
+    static __device__ __forceinline__ uint32_t finish(uint32_t w) {
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&w), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    template <uint32_t A, uint32_t B>
+    static __device__ __forceinline__ void two(uint32_t x, uint32_t &a, uint32_t &b) {
+        x ^= 0x80808080u;
+        a = finish(__byte_perm(x, 0x64646464u, A));
+        b = finish(__byte_perm(x, 0x64646464u, B));
+    }
+    static __device__ __forceinline__ void near(uint32_t x, uint32_t &a, uint32_t &b) { two<0x4140, 0x4342>(x, a, b); }
+    static __device__ __forceinline__ void apart(uint32_t x, uint32_t &a, uint32_t &b) { two<0x4240, 0x4341>(x, a, b); }
+};
+template <>
+struct AtCode<true> {
+    static constexpr float kUnit = 256.f;
+    static __device__ __forceinline__ uint32_t finish(uint32_t w) {
+        return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+    }
+    static __device__ __forceinline__ void near(uint32_t x, uint32_t &a, uint32_t &b) {
+        a = finish(__byte_perm(x, 0u, 0x1404));
+        b = finish(__byte_perm(x, 0u, 0x3424));
+    }
+    static __device__ __forceinline__ void apart(uint32_t x, uint32_t &a, uint32_t &b) {
+        a = finish(__byte_perm(x, 0u, 0x2404));
+        b = finish(__byte_perm(x, 0u, 0x3414));
+    }
+};
+
+// ------------------------------------------------------- the line of steps
+
+// Steps of row tile rt of a sequence: [s0, s0 + n); a tile that sees no key has
+// one step, all of it masked.
+struct AtTile {
+    int s0, n;
+};
+__device__ __forceinline__ AtTile at_tile(const KvSeq &s, int rt, int rows, int G, int window) {
+    const int r0 = rt * rows, r1 = min(r0 + rows, s.n * G) - 1;
+    const int hi = s.len - s.n + r1 / G;
+    const int lo = window > 0 ? max(0, s.len - s.n + r0 / G - window + 1) : 0;
+    AtTile t;
+    t.s0 = hi < lo ? 0 : lo / kAtStep;
+    t.n = hi < lo ? 1 : hi / kAtStep - t.s0 + 1;
+    return t;
+}
+__device__ __forceinline__ int at_tiles(const KvSeq &s, int rows, int G) { return (s.n * G + rows - 1) / rows; }
+__device__ __forceinline__ long long at_seq_steps(const KvSeq &s, int rows, const AttendParams &p) {
+    long long w = 0;
+    for (int rt = 0, n = at_tiles(s, rows, p.G); rt < n; ++rt) w += at_tile(s, rt, rows, p.G, p.window).n;
+    return w * p.H;
+}
+
+// A CTA's part of the line, walked item by item; uniform over a warp.
+struct AtWalk {
+    long long total, at, end;          // steps of the line, the next one, this part's end
+    int parts;                         // CTAs that take a part
+    int b, rt, nrt, h;                 // the item
+    KvSeq seq;
+    AtTile tile;
+    int off;                           // steps of the item that lie before `at`
+
+    __device__ __forceinline__ int piece() const { return (int)min((long long)(tile.n - off), end - at); }
+
+    __device__ __forceinline__ void init(const AttendParams &p, int rows, bool &bad) {
+        const int lane = threadIdx.x & 31;
+        total = 0;
+        for (int b0 = 0; b0 < p.tok.B; b0 += 32) {
+            long long w = 0;
+            if (b0 + lane < p.tok.B) w = at_seq_steps(kv_seq(p.tok, b0 + lane, bad), rows, p);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            total += w;
+        }
+        parts = (int)min((long long)gridDim.x, (total + p.min_steps - 1) / p.min_steps);
+        const int c = blockIdx.x;
+        at = end = 0;
+        if (c >= parts) return;
+        at = total * c / parts;
+        end = total * (c + 1) / parts;
+        long long before = 0;
+        for (int b0 = 0; b0 < p.tok.B; b0 += 32) {
+            long long w = 0;
+            if (b0 + lane < p.tok.B) w = at_seq_steps(kv_seq(p.tok, b0 + lane, bad), rows, p);
+            long long sum = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const unsigned who = __ballot_sync(0xffffffffu, at >= before + sum - w && at < before + sum);
+            if (who) {
+                const int src = __ffs(who) - 1;
+                b = b0 + src;
+                before += __shfl_sync(0xffffffffu, sum - w, src);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        seq = kv_seq(p.tok, b, bad);
+        nrt = at_tiles(seq, rows, p.G);
+        long long left = at - before;
+        for (rt = 0;; ++rt) {
+            tile = at_tile(seq, rt, rows, p.G, p.window);
+            if (left < (long long)tile.n * p.H || rt + 1 >= nrt) break;
+            left -= (long long)tile.n * p.H;
+        }
+        h = (int)(left / tile.n);
+        off = (int)(left - (long long)h * tile.n);
+    }
+    // past the current piece of n steps
+    __device__ __forceinline__ void next(const AttendParams &p, int rows, int n, bool &bad) {
+        at += n;
+        off = 0;
+        if (at >= end) return;
+        if (++h < p.H) return;
+        h = 0;
+        if (++rt >= nrt) {
+            rt = 0;
+            do seq = kv_seq(p.tok, ++b, bad);
+            while (seq.n == 0 && b + 1 < p.tok.B);
+            nrt = at_tiles(seq, rows, p.G);
+        }
+        tile = at_tile(seq, rt, rows, p.G, p.window);
+    }
+    // the part that holds step s of the line
+    __device__ __forceinline__ int part_of(long long s) const { return (int)(((s + 1) * parts - 1) / total); }
+};
+
+// --------------------------------------------------------------- the kernel
+
+// What the streaming warp leaves beside a step's codes, for each half (16
+// tokens) of the step: the score's factor, log2 of the value scale, and one
+// over it; factor < 0 marks tokens that are not there.
+struct AtScales {
+    float sk[2], lsv[2], rsv[2];
+    float pad[2];
+};
+
+template <int D, int NT, int WR, int WARPS>
+struct AtShape {
+    static constexpr int kRows = 8 * NT * WR;              // rows of an item
+    static constexpr int kGroups = WARPS / WR;             // warps that take different steps
+    static constexpr int kStepBytes = 2 * kAtStep * D;
+    static constexpr int kThreads = 32 * (WARPS + 1);
+    static constexpr bool kQShared = NT > 1;               // queries in shared memory (else registers)
+    static constexpr int kQStride = D + 16;                // halves; 8 g + 2 c words: no conflicts
+    static constexpr int kOStride = D + 4;                 // floats; 8 c + 2 g words: no conflicts
+    static constexpr size_t kQBytes = kQShared ? (size_t)kRows * kQStride * 2 : 0;
+    static constexpr size_t kOBytes = (size_t)kGroups * kRows * kOStride * 4;
+    static constexpr size_t kMlBytes = (size_t)kGroups * kRows * 8;
+    static size_t smem(int stages) {
+        return 1024 + (size_t)stages * (kStepBytes + sizeof(AtScales) + 16) + kQBytes + kOBytes + kMlBytes + kRows * 4 + 64;
+    }
+};
+
+template <int D, int NT, int WR, int WARPS, bool E4M3>
+__global__ void __launch_bounds__(32 * (WARPS + 1))
+    eva_attend_kernel(const __grid_constant__ AttendMaps maps, AttendParams p, int stages) {
+    using S = AtShape<D, NT, WR, WARPS>;
+    constexpr int kRows = S::kRows, kGroups = S::kGroups, kChunks = D / 16;
+    constexpr int kBarConsumers = 1;
+    // shared memory: ring | scales | full and free barriers | queries | outputs | statistics
+    const uint32_t base0 = (uint32_t)__cvta_generic_to_shared(eva_smem);
+    const uint32_t skip = ((base0 + 1023) & ~1023u) - base0;
+    uint8_t *ring = eva_smem + skip;
+    const uint32_t ring_a = base0 + skip;
+    AtScales *scales = reinterpret_cast<AtScales *>(ring + (size_t)stages * S::kStepBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + stages);
+    const uint32_t full_a = (uint32_t)__cvta_generic_to_shared(bars), free_a = full_a + 8 * stages;
+    __half *qs = reinterpret_cast<__half *>(bars + 2 * stages);
+    float *os = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(qs) + S::kQBytes);
+    float2 *mls = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(os) + S::kOBytes);
+    // [0] this CTA joins the item, [1] a warp of this CTA gave up a wait
+    volatile int *flag = reinterpret_cast<volatile int *>(reinterpret_cast<uint8_t *>(mls) + S::kMlBytes);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(full_a + 8 * i, 1);
+            mbar_init(free_a + 8 * i, WR);
+        }
+        flag[1] = 0;
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch();
+    bool bad = false;
+    AtWalk walk;
+    walk.init(p, kRows, bad);
+
+    if (warp == WARPS) {
+        // ------------------------------------------------ the streaming warp
+        const int page = p.tok.page, boxes = page < kAtStep ? 2 : 1;     // boxes of a step
+        const int box_rows = kAtStep / boxes;
+        int t = 0;
+        bool ok = !p.inject;
+        while (walk.at < walk.end && ok) {
+            const int n = walk.piece(), s_first = walk.tile.s0 + walk.off;
+            const long long row = (long long)walk.b * p.tok.max_pages;
+            for (int s0 = 0; s0 < n && ok; s0 += 32) {
+                // each lane looks up one step: its pages (-1: no token there) and their scales
+                int pid[2] = {-1, -1};
+                float sk[2] = {-1.f, -1.f}, sv[2] = {1.f, 1.f};
+                if (s0 + lane < n) {
+                    const int tok0 = (s_first + s0 + lane) * kAtStep;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (i == 1 && boxes == 1) {
+                            if (tok0 + 16 < walk.seq.len) pid[1] = pid[0];
+                        } else if (tok0 + 16 * i < walk.seq.len) {
+                            pid[i] = p.tok.table[row + (tok0 + 16 * i) / page];
+                            if (pid[i] < 0 || pid[i] >= p.tok.num_pages) {
+                                bad = true;
+                                pid[i] = -1;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (pid[i] < 0) continue;
+                        sk[i] = p.k_scale[(long long)pid[i] * p.H + walk.h];
+                        sv[i] = p.v_scale[(long long)pid[i] * p.H + walk.h];
+                    }
+                }
+                const int steps = min(32, n - s0);
+                for (int i = 0; i < steps; ++i, ++t) {
+                    const int st = t % stages, round = t / stages;
+                    if (round > 0 && !mbar_wait_bounded(free_a + 8 * st, (round - 1) & 1, p.wait_rounds)) {
+                        ok = false;
+                        break;
+                    }
+                    const int p0 = __shfl_sync(0xffffffffu, pid[0], i), p1 = __shfl_sync(0xffffffffu, pid[1], i);
+                    const float k0 = __shfl_sync(0xffffffffu, sk[0], i), k1 = __shfl_sync(0xffffffffu, sk[1], i);
+                    const float v0 = __shfl_sync(0xffffffffu, sv[0], i), v1 = __shfl_sync(0xffffffffu, sv[1], i);
+                    if (lane == 0) {
+                        const uint32_t bar = full_a + 8 * st, dst = ring_a + st * S::kStepBytes;
+                        const int live = (p0 >= 0) + (boxes == 2 && p1 >= 0);
+                        AtScales &sc = scales[st];
+                        const float e0 = fmaxf(v0 * AtCode<E4M3>::kUnit, 1e-30f), e1 = fmaxf(v1 * AtCode<E4M3>::kUnit, 1e-30f);
+                        sc.sk[0] = p0 < 0 ? -1.f : k0 * AtCode<E4M3>::kUnit;
+                        sc.sk[1] = p1 < 0 ? -1.f : k1 * AtCode<E4M3>::kUnit;
+                        sc.lsv[0] = log2f(e0);
+                        sc.lsv[1] = log2f(e1);
+                        sc.rsv[0] = 1.f / e0;
+                        sc.rsv[1] = 1.f / e1;
+                        if (live)
+                            mbar_arrive_expect_tx(bar, (uint32_t)(live * 2 * box_rows * D));
+                        else
+                            mbar_arrive(bar);
+                        const int slot = (s_first + s0 + i) * kAtStep % page;
+#pragma unroll
+                        for (int bx = 0; bx < 2; ++bx) {
+                            const int id = bx ? p1 : p0;
+                            if (bx >= boxes || id < 0) continue;
+                            const int y = (id * p.H + walk.h) * page + (boxes == 2 ? 0 : slot);
+#pragma unroll
+                            for (int x = 0; x < D; x += 128) {     // a column half of 128 bytes is [32][128]
+                                const uint32_t o = dst + (uint32_t)(x * kAtStep + bx * box_rows * (D < 128 ? D : 128));
+                                at_tma_2d(o, &maps.k, x, y, bar);
+                                at_tma_2d(o + kAtStep * D, &maps.v, x, y, bar);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            walk.next(p, kRows, n, bad);
+        }
+        if (bad) atomicOr(p.status, kKvStatusIndex);
+        if (!ok) {                     // a consumer gave up: record it, let the copies in flight land
+            if (lane == 0) atomicOr(p.status, kAtStatusWait);
+            for (int i = max(0, t - stages); i < t; ++i)
+                mbar_wait_bounded(full_a + 8 * (i % stages), (i / stages) & 1, p.wait_rounds);
+        }
+        return;
+    }
+
+    // ------------------------------------------------------------ consumers
+    const int wr = warp % WR, grp = warp / WR;
+    const int g = lane >> 2, c = lane & 3, tid = threadIdx.x;      // tid < 32 * WARPS
+    constexpr float kLog2e = 1.4426950408889634f;
+    const float zscale = p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e;
+    const float zcap = p.cap * kLog2e;
+    int t0 = 0;
+    bool ok = true;
+    while (walk.at < walk.end && ok) {
+        const int n = walk.piece(), s_first = walk.tile.s0 + walk.off;
+        const KvSeq seq = walk.seq;
+        const int r0 = walk.rt * kRows, nrows = min(kRows, seq.n * p.G - r0);
+        // queries
+        uint32_t qf[S::kQShared ? 1 : kChunks][2];
+        auto qrow = [&](int r) {       // r: row of the item
+            const int i = (r0 + r) / p.G, hq = walk.h * p.G + (r0 + r) - i * p.G;
+            return p.q + (seq.row + i) * p.ldq + (long long)hq * D;
+        };
+        if constexpr (S::kQShared) {
+            for (int i = tid; i < kRows * (D / 8); i += 32 * WARPS) {
+                const int r = i / (D / 8), x = i - r * (D / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < nrows) v = reinterpret_cast<const uint4 *>(qrow(r))[x];
+                *reinterpret_cast<uint4 *>(qs + r * S::kQStride + x * 8) = v;
+            }
+            asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
+        } else {
+            const bool live = wr * 8 + g < nrows;
+            const __half *src = live ? qrow(wr * 8 + g) : nullptr;
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) {
+                uint2 v = make_uint2(0, 0);
+                if (live) v = *reinterpret_cast<const uint2 *>(src + ch * 16 + 4 * c);
+                qf[ch][0] = v.x;
+                qf[ch][1] = v.y;
+            }
+        }
+        // positions: the last key each of this lane's rows sees
+        int last[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                last[nt][e] = seq.len - seq.n + (r0 + min(nrows - 1, (wr * NT + nt) * 8 + 2 * c + e)) / p.G;
+        const int pmin = seq.len - seq.n + r0 / p.G;                       // of the item's first row
+        const int pmax = seq.len - seq.n + (r0 + nrows - 1) / p.G;
+
+        float o[NT][kChunks][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][ch][e] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+        }
+
+        for (int i = ((grp - t0) % kGroups + kGroups) % kGroups; i < n; i += kGroups) {
+            const int t = t0 + i, st = t % stages;
+            if (!mbar_wait_bounded(full_a + 8 * st, (t / stages) & 1, p.wait_rounds)) {
+                if (lane == 0) flag[1] = 1;
+                break;
+            }
+            const uint32_t kt = ring_a + st * S::kStepBytes, vt = kt + kAtStep * D;
+            const AtScales sc = scales[st];
+            // S^T = K Q^T: 32 tokens x 8 NT rows
+            float z[NT][2][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[nt][mt][e] = 0.f;
+            auto addr = [&](uint32_t tile, int tok, int ch) {
+                if constexpr (D >= 128)
+                    return tile + (uint32_t)((ch >> 3) * (kAtStep * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                else
+                    return tile + (uint32_t)(tok * 64 + ((ch ^ ((tok >> 1) & 3)) << 4));
+            };
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ch += 2) {
+                uint32_t a[2][2][4];   // [half of the tokens][chunk][fragment]
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    uint32_t r[4];
+                    at_ldsm(addr(kt, mt * 16 + (lane & 15), ch + (lane >> 4)), r);
+                    AtCode<E4M3>::near(r[0], a[mt][0][0], a[mt][0][2]);
+                    AtCode<E4M3>::near(r[1], a[mt][0][1], a[mt][0][3]);
+                    AtCode<E4M3>::near(r[2], a[mt][1][0], a[mt][1][2]);
+                    AtCode<E4M3>::near(r[3], a[mt][1][1], a[mt][1][3]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t b0, b1;
+                        if constexpr (S::kQShared) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(
+                                qs + ((wr * NT + nt) * 8 + g) * S::kQStride + (ch + x) * 16 + 4 * c);
+                            b0 = v.x;
+                            b1 = v.y;
+                        } else {
+                            b0 = qf[ch + x][0];
+                            b1 = qf[ch + x][1];
+                        }
+                        at_mma(z[nt][0], a[0][x], b0, b1);
+                        at_mma(z[nt][1], a[1][x], b0, b1);
+                    }
+                }
+            }
+            // scores, in base 2 and with the value scale's logarithm added
+            const int tok0 = (s_first + i) * kAtStep;
+            const bool edge = tok0 + kAtStep - 1 > pmin || (p.window > 0 && tok0 <= pmax - p.window) ||
+                              sc.sk[0] < 0.f || sc.sk[1] < 0.f;
+            uint32_t pb[NT][2][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = z[nt][mt][e] * (sc.sk[mt] * zscale);
+                        if (p.cap > 0.f) x = zcap * (1.f - 2.f / (1.f + __expf(2.f * x)));
+                        z[nt][mt][e] = x + sc.lsv[mt];
+                    }
+                if (edge) {
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = tok0 + mt * 16 + g + (e >> 1) * 8, pos = last[nt][e & 1];
+                            if (j > pos || (p.window > 0 && j <= pos - p.window) || sc.sk[mt] < 0.f)
+                                z[nt][mt][e] = -INFINITY;
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(fmaxf(z[nt][0][e], z[nt][0][e + 2]), fmaxf(z[nt][1][e], z[nt][1][e + 2]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    const float mn = fmaxf(m[nt][e], mx);
+                    const float ref = mn == -INFINITY ? 0.f : mn;
+                    if (__any_sync(0xffffffffu, mn > m[nt][e])) {
+                        const float f = at_exp2(m[nt][e] - ref);       // 0 for the first keys
+                        l[nt][e] *= f;
+#pragma unroll
+                        for (int ch = 0; ch < kChunks; ++ch) {
+                            o[nt][ch][e] *= f;
+                            o[nt][ch][e + 2] *= f;
+                        }
+                        m[nt][e] = mn;
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const float w0 = at_exp2(z[nt][mt][e] - ref), w1 = at_exp2(z[nt][mt][e + 2] - ref);
+                        z[nt][mt][e] = w0;
+                        z[nt][mt][e + 2] = w1;
+                        l[nt][e] += (w0 + w1) * sc.rsv[mt];
+                    }
+                }
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const __half2 w = __floats2half2_rn(z[nt][mt][2 * e], z[nt][mt][2 * e + 1]);
+                        pb[nt][mt][e] = at_transpose(*reinterpret_cast<const uint32_t *>(&w));
+                    }
+            }
+            // O^T += V^T P^T
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) {
+                uint32_t r[4], a[2][4];
+                at_ldsm_t(addr(vt, lane, ch), r);
+                AtCode<E4M3>::apart(r[0], a[0][0], a[0][1]);
+                AtCode<E4M3>::apart(r[1], a[0][2], a[0][3]);
+                AtCode<E4M3>::apart(r[2], a[1][0], a[1][1]);
+                AtCode<E4M3>::apart(r[3], a[1][2], a[1][3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    at_mma(o[nt][ch], a[0], pb[nt][0][0], pb[nt][0][1]);
+                    at_mma(o[nt][ch], a[1], pb[nt][1][0], pb[nt][1][1]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(free_a + 8 * st);
+        }
+        // this piece's sums: the warps of different steps meet in shared memory
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+                const int r = (wr * NT + nt) * 8 + 2 * c + e;
+                if (g == 0) mls[grp * kRows + r] = make_float2(m[nt][e], l[nt][e]);
+                float *dst = os + (size_t)(grp * kRows + r) * S::kOStride + 2 * g;
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch)
+                    *reinterpret_cast<float2 *>(dst + ch * 16) = make_float2(o[nt][ch][e], o[nt][ch][e + 2]);
+            }
+        asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
+        ok = flag[1] == 0;             // the same answer in every warp: nothing sets it before the barrier below
+        const bool whole = n == walk.tile.n;
+        const long long lo = walk.at - walk.off;             // the item's first step of the line
+        const int slot = walk.off > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1;
+        auto emit = [&](int r, int x, const float4 &v, float mm, float ll) {
+            const int i = (r0 + r) / p.G, hq = walk.h * p.G + (r0 + r) - i * p.G;
+            const float f = ll > 0.f ? 1.f / ll : 0.f;
+            const long long at = ((long long)(seq.row + i) * p.Hq + hq) * D + x;
+            if (p.out_f32) {
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
+                    make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            } else {
+                const __half2 a = __floats2half2_rn(v.x * f, v.y * f), b = __floats2half2_rn(v.z * f, v.w * f);
+                *reinterpret_cast<uint2 *>(static_cast<__half *>(p.out) + at) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+            }
+            if (p.lse && x == 0)
+                p.lse[(long long)(seq.row + i) * p.Hq + hq] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        };
+        for (int i = tid; i < nrows * (D / 4); i += 32 * WARPS) {
+            const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+            float mm = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kGroups; ++w) mm = fmaxf(mm, mls[w * kRows + r].x);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            float ll = 0.f;
+#pragma unroll
+            for (int w = 0; w < kGroups; ++w) {
+                const float2 ml = mls[w * kRows + r];
+                const float f = at_exp2(ml.x - ref);
+                const float4 y = *reinterpret_cast<const float4 *>(os + (size_t)(w * kRows + r) * S::kOStride + x);
+                v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
+                ll += ml.y * f;
+            }
+            if (whole) {
+                emit(r, x, v, mm, ll);
+            } else {
+                reinterpret_cast<float4 *>(p.part)[((size_t)slot * kRows + r) * (D / 4) + x / 4] = v;
+                if (x == 0) p.part_ml[(size_t)slot * kRows + r] = make_float2(mm, ll);
+            }
+        }
+        if (!whole) {
+            // the last part of the item to finish joins them all
+            const int c0 = walk.part_of(lo), c1 = walk.part_of(lo + walk.tile.n - 1);
+            __threadfence();
+            asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
+            if (tid == 0) {
+                const int old = atomicAdd(p.counters + c0, 1);
+                flag[0] = old == c1 - c0;
+                if (flag[0]) p.counters[c0] = 0;
+                __threadfence();
+            }
+            asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
+            if (flag[0]) {
+                for (int i = tid; i < nrows * (D / 4); i += 32 * WARPS) {
+                    const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+                    float mm = -INFINITY;
+                    for (int cc = c0; cc <= c1; ++cc)
+                        mm = fmaxf(mm, __ldcg(p.part_ml + (size_t)(2 * cc + (cc == c0)) * kRows + r).x);
+                    const float ref = mm == -INFINITY ? 0.f : mm;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float ll = 0.f;
+                    for (int cc = c0; cc <= c1; ++cc) {
+                        const size_t sl = 2 * cc + (cc == c0);
+                        const float2 ml = __ldcg(p.part_ml + sl * kRows + r);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part) + (sl * kRows + r) * (D / 4) + x / 4);
+                        const float f = at_exp2(ml.x - ref);
+                        v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
+                        ll += ml.y * f;
+                    }
+                    emit(r, x, v, mm, ll);
+                }
+            }
+        }
+        asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
+        t0 += n;
+        walk.next(p, kRows, n, bad);
+    }
+    if (!ok && lane == 0) atomicOr(p.status, kAtStatusWait);
+}
+
+}  // namespace eva

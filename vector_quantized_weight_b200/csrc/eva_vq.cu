@@ -765,6 +765,7 @@ const char *eva_vq_status_string(eva_status_t s) {
         case EVA_ERR_DEVICE_CHECK: return "device-side bounds check failed (checked build)";
         case EVA_ERR_SCRATCH_TOO_SMALL:
             return "B * K * 4 bytes exceed the 4 MiB static scratch of eva_vq_linear_run_noalloc";
+        case EVA_ERR_BAD_INDEX: return "an index on the device (row start, length or page) was out of range";
     }
     return "unknown status";
 }
@@ -1806,3 +1807,5 @@ eva_status_t eva_vq_quantize(const eva_quant_desc *desc, const void *w, const in
 }
 
 }  // extern "C"
+
+#include "eva_attn_host.cuh"

@@ -13,8 +13,12 @@ import os
 from . import build as _build
 
 EVA_OK, EVA_ERR_INVALID_ARG, EVA_ERR_UNSUPPORTED, EVA_ERR_CUDA, EVA_ERR_OOM, \
-    EVA_ERR_DEVICE_TIMEOUT, EVA_ERR_NO_DEVICE, EVA_ERR_DEVICE_CHECK, EVA_ERR_SCRATCH_TOO_SMALL = range(9)
+    EVA_ERR_DEVICE_TIMEOUT, EVA_ERR_NO_DEVICE, EVA_ERR_DEVICE_CHECK, EVA_ERR_SCRATCH_TOO_SMALL, \
+    EVA_ERR_BAD_INDEX = range(10)
 EVA_F16, EVA_F32 = 0, 1
+EVA_ROPE_HALF, EVA_ROPE_INTERLEAVED = 0, 1
+EVA_ROPE_UNSCALED, EVA_ROPE_LINEAR, EVA_ROPE_NTK, EVA_ROPE_YARN, EVA_ROPE_BANDS = range(5)
+EVA_CACHE_INT8, EVA_CACHE_E4M3 = 0, 1
 EVA_PATH_AUTO, EVA_PATH_OC_LOOKUP, EVA_PATH_DEQUANT_MMA, EVA_PATH_TCGEN05 = 0, 1, 2, 3
 
 # Every function the header declares; the CPU tests check the library exports them.
@@ -27,6 +31,9 @@ ABI_FUNCTIONS = (
     "eva_vq_debug_timeline", "eva_vq_linear_run_noalloc",
     "eva_vq_quantize", "eva_vq_kmeans_assign", "eva_vq_kmeans_update", "eva_vq_residual",
     "eva_vq_linear_run_group", "eva_vq_debug_inject_wait_timeout",
+    "eva_rope_create", "eva_rope_run", "eva_rope_destroy",
+    "eva_kv_create", "eva_kv_append", "eva_kv_read", "eva_kv_attend", "eva_kv_sync_status",
+    "eva_kv_debug_inject_wait_timeout", "eva_kv_cache_info", "eva_kv_destroy",
 )
 
 
@@ -60,6 +67,27 @@ class eva_vq_info(ctypes.Structure):
                 ("grid", ctypes.c_int32), ("kernels_per_run", ctypes.c_int32),
                 ("path", ctypes.c_int32), ("sm_count", ctypes.c_int32),
                 ("staged_units", ctypes.c_int32)]
+
+
+class eva_rope_desc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("scaling", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class eva_kv_desc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("cache_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int),
+                ("window", ctypes.c_int32), ("softcap", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class eva_kv_info(ctypes.Structure):
+    _fields_ = [("workspace_bytes", ctypes.c_int64), ("sm_count", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("grid", ctypes.c_int32), ("stages", ctypes.c_int32)]
 
 
 _lib = None
@@ -114,6 +142,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.eva_vq_kmeans_assign.argtypes = [P, I64, I32, P, I32, I64, P, P]
     lib.eva_vq_kmeans_update.argtypes = [P, I64, I32, P, I32, I64, P, P, P, P]
     lib.eva_vq_residual.argtypes = [P, I32, I32, P, I32, P, I32, I32, P, P, P]
+    lib.eva_rope_create.argtypes = [ctypes.POINTER(H), ctypes.POINTER(eva_rope_desc), P, P, P]
+    lib.eva_rope_run.argtypes = [H, P, I64, P, I64, P, I32, P, I64, P, I64, P]
+    lib.eva_rope_destroy.argtypes = [H]
+    lib.eva_kv_create.argtypes = [ctypes.POINTER(H), ctypes.POINTER(eva_kv_desc), P, P, P, P, P]
+    lib.eva_kv_append.argtypes = [H, P, I64, P, I64, ctypes.c_int, P, P, P, I32, I32, P]
+    lib.eva_kv_read.argtypes = [H, P, P, P, I32, I32, ctypes.c_int, P, P, P]
+    lib.eva_kv_attend.argtypes = [H, P, I64, P, P, P, I32, I32, P, P, P]
+    lib.eva_kv_sync_status.argtypes = [H]
+    lib.eva_kv_debug_inject_wait_timeout.argtypes = [H, I32]
+    lib.eva_kv_cache_info.argtypes = [H, ctypes.POINTER(eva_kv_info)]
+    lib.eva_kv_destroy.argtypes = [H]
     for fn in ABI_FUNCTIONS:
         if fn != "eva_vq_status_string":
             getattr(lib, fn).restype = ctypes.c_int
@@ -228,6 +267,62 @@ def eva_vq_residual(wrot: int, N: int, K: int, wc: int, ncent: int, wi: int, cod
                     signs_out: int, alpha_out: int, stream: int | None) -> None:
     _check("eva_vq_residual", load().eva_vq_residual(wrot, int(N), int(K), wc, int(ncent), wi,
                                                      int(codebook_rows), int(group), signs_out, alpha_out, stream))
+
+
+def eva_rope_create(desc: eva_rope_desc, q_weight: int | None, k_weight: int | None, stream: int | None) -> int:
+    h = ctypes.c_void_p()
+    _check("eva_rope_create", load().eva_rope_create(ctypes.byref(h), ctypes.byref(desc), q_weight, k_weight, stream))
+    return h.value
+
+
+def eva_rope_run(h: int, q: int | None, ldq: int, k: int | None, ldk: int, positions: int | None, T: int,
+                 q_out: int | None, ldqo: int, k_out: int | None, ldko: int, stream: int | None) -> None:
+    _check("eva_rope_run", load().eva_rope_run(h, q, ldq, k, ldk, positions, T, q_out, ldqo, k_out, ldko, stream))
+
+
+def eva_rope_destroy(h: int | None) -> None:
+    _check("eva_rope_destroy", load().eva_rope_destroy(h))
+
+
+def eva_kv_create(desc: eva_kv_desc, k_pages: int, v_pages: int, k_scale: int, v_scale: int,
+                  stream: int | None) -> int:
+    h = ctypes.c_void_p()
+    _check("eva_kv_create", load().eva_kv_create(ctypes.byref(h), ctypes.byref(desc), k_pages, v_pages, k_scale,
+                                                 v_scale, stream))
+    return h.value
+
+
+def eva_kv_append(h: int, k: int, ldk: int, v: int, ldv: int, in_dtype: int, starts: int, lens: int,
+                  page_table: int, B: int, T: int, stream: int | None) -> None:
+    _check("eva_kv_append", load().eva_kv_append(h, k, ldk, v, ldv, in_dtype, starts, lens, page_table, B, T, stream))
+
+
+def eva_kv_read(h: int, starts: int, begins: int, page_table: int, B: int, T: int, out_dtype: int,
+                k_out: int | None, v_out: int | None, stream: int | None) -> None:
+    _check("eva_kv_read", load().eva_kv_read(h, starts, begins, page_table, B, T, out_dtype, k_out, v_out, stream))
+
+
+def eva_kv_attend(h: int, q: int, ldq: int, starts: int, lens: int, page_table: int, B: int, T: int, out: int,
+                  lse: int | None, stream: int | None) -> None:
+    _check("eva_kv_attend", load().eva_kv_attend(h, q, ldq, starts, lens, page_table, B, T, out, lse, stream))
+
+
+def eva_kv_sync_status(h: int) -> int:
+    return int(load().eva_kv_sync_status(h))
+
+
+def eva_kv_debug_inject_wait_timeout(h: int, rounds: int) -> None:
+    _check("eva_kv_debug_inject_wait_timeout", load().eva_kv_debug_inject_wait_timeout(h, rounds))
+
+
+def eva_kv_cache_info(h: int) -> eva_kv_info:
+    info = eva_kv_info()
+    _check("eva_kv_cache_info", load().eva_kv_cache_info(h, ctypes.byref(info)))
+    return info
+
+
+def eva_kv_destroy(h: int | None) -> None:
+    _check("eva_kv_destroy", load().eva_kv_destroy(h))
 
 
 # ------------------------------------------------------- torch convenience
@@ -364,3 +459,278 @@ def run_group(layers, xs, outs=None, stream=None, independent=False):
     eva_vq_linear_run_group([l.handle for l in layers], [x.data_ptr() for x in xs], [y.data_ptr() for y in outs],
                             B, _stream_handle(stream), EVA_RUN_INDEPENDENT if independent else 0)
     return outs
+
+
+# ------------------------------- between a block's q, k, v layers and its o layer
+
+_DTYPES = {}      # torch dtype or its name -> (torch dtype, eva_dtype_t); filled on first use
+
+
+def _dtype(t):
+    if not _DTYPES:
+        import torch
+        for d, code in ((torch.float16, EVA_F16), (torch.float32, EVA_F32)):
+            _DTYPES[d] = _DTYPES[str(d).removeprefix("torch.")] = (d, code)
+    if t not in _DTYPES:
+        raise ValueError(f"dtype must be float16 or float32, not {t}")
+    return _DTYPES[t]
+
+
+def _rows(name, x, heads, head_dim, dtype, device):
+    """Checks a [T][heads][head_dim] (or [T][heads * head_dim]) tensor whose rows may lie apart; (T, row stride)."""
+    shape, stride = x.shape, x.stride()
+    if x.dtype != dtype or x.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor on {device}, not {x.dtype} on {x.device}")
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == head_dim and (
+            (stride[2] == 1 or head_dim == 1) and (stride[1] == head_dim or heads == 1) or 0 in shape)
+    else:
+        ok = len(shape) == 2 and shape[1] == heads * head_dim and (stride[1] == 1 or shape[1] <= 1 or 0 in shape)
+    if not ok:
+        raise ValueError(f"{name} must be [T][{heads}][{head_dim}] with contiguous rows, not {tuple(shape)} "
+                         f"with strides {stride}")
+    return shape[0], (stride[0] if shape[0] > 1 else heads * head_dim)
+
+
+def _indices(name, x, shape, device):
+    if x.dtype != _INT32() or x.device != device or x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}, "
+                         f"not {x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+def _INT32():
+    import torch
+    return torch.int32
+
+
+class _OnDevice:
+    """A handle on one device: its stream, and outputs that belong to the stream of the call."""
+
+    def _stream(self, stream):
+        import torch
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        if stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the handle on {self.device}")
+        return stream.cuda_stream
+
+    def _empty(self, shape, dtype, stream):
+        import torch
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class HeadRope(_OnDevice):
+    """Rotary positions for a block's queries and keys, with the per-head RMS norm in the same pass (norm=True).
+
+    layout: "half" (dimensions i and i + rotary_dim / 2 turn together) or "interleaved" (2i and 2i + 1);
+    rotary_dim (default head_dim): the first dimensions of a head, the others pass through.
+    scaling: None or {"type": "linear" | "ntk" | "yarn" | "bands", "factor": f, ...}; yarn takes "original", "low"
+    (1) and "high" (32), bands "original", "low" (1) and "high" (4); "magnitude" replaces the type's own (see the
+    header for the formulas).  q_weight, k_weight: CUDA fp16 [head_dim], copied; weight_offset is added to them."""
+
+    _SCALING = {"linear": EVA_ROPE_LINEAR, "ntk": EVA_ROPE_NTK, "yarn": EVA_ROPE_YARN, "bands": EVA_ROPE_BANDS}
+
+    def __init__(self, q_heads, kv_heads, head_dim, *, rotary_dim=None, layout="half", theta=10000.0, scaling=None,
+                 norm=False, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, in_dtype="float16",
+                 out_dtype="float16", device=None, stream=None):
+        import torch
+        self.handle = None
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
+        self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
+        self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
+        self.in_dtype, code_in = _dtype(in_dtype)
+        self.out_dtype, code_out = _dtype(out_dtype)
+        how = dict(scaling or {"type": "none"})
+        kind = how.pop("type", None)
+        if kind != "none" and kind not in self._SCALING:
+            raise ValueError(f"scaling type must be one of {sorted(self._SCALING)}, not {kind!r}")
+        unknown = set(how) - {"factor", "original", "low", "high", "magnitude"}
+        if unknown:
+            raise ValueError(f"unknown scaling entries {sorted(unknown)}")
+        self.device = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index or 0)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None and (w.dtype != torch.float16 or w.device != self.device or
+                                  tuple(w.shape) != (self.head_dim,) or not w.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous float16 tensor ({self.head_dim},) on {self.device}")
+        self.desc = eva_rope_desc(self.q_heads, self.kv_heads, self.head_dim, self.rotary_dim,
+                                  EVA_ROPE_HALF if layout == "half" else EVA_ROPE_INTERLEAVED, int(bool(norm)), code_in,
+                                  code_out, self._SCALING.get(kind, EVA_ROPE_UNSCALED), float(eps), float(weight_offset),
+                                  float(theta), float(how.get("factor", 1.0)), float(how.get("original", 0.0)),
+                                  float(how.get("low", 1.0)), float(how.get("high", 4.0 if kind == "bands" else 32.0)),
+                                  float(how.get("magnitude", 0.0)))
+        with torch.cuda.device(self.device):
+            self.handle = eva_rope_create(self.desc, _ptr(q_weight), _ptr(k_weight), self._stream(stream))
+        self._run = load().eva_rope_run
+
+    def __call__(self, q, k, positions, q_out=None, k_out=None, stream=None):
+        """(q_out, k_out) of q [T][q_heads][head_dim], k [T][kv_heads][head_dim] (rows may lie apart, as columns of
+        a fused projection) and positions int32 [T].  q_out=q, k_out=k write in place when the types are equal."""
+        Hq, Hk, D, dev = self.q_heads, self.kv_heads, self.head_dim, self.device
+        T, ldq = _rows("q", q, Hq, D, self.in_dtype, dev)
+        Tk, ldk = _rows("k", k, Hk, D, self.in_dtype, dev)
+        if T != Tk:
+            raise ValueError(f"q has {T} rows, k has {Tk}")
+        if self.rotary_dim or positions is not None:
+            _indices("positions", positions, (T,), dev)
+        if q_out is None:
+            q_out, ldqo = self._empty((T, Hq, D), self.out_dtype, stream), Hq * D
+        else:
+            To, ldqo = _rows("q_out", q_out, Hq, D, self.out_dtype, dev)
+            if To != T:
+                raise ValueError(f"q_out has {To} rows, q has {T}")
+        if k_out is None:
+            k_out, ldko = self._empty((T, Hk, D), self.out_dtype, stream), Hk * D
+        else:
+            To, ldko = _rows("k_out", k_out, Hk, D, self.out_dtype, dev)
+            if To != T:
+                raise ValueError(f"k_out has {To} rows, k has {T}")
+        rc = self._run(self.handle, q.data_ptr(), ldq, k.data_ptr(), ldk,
+                       None if positions is None else positions.data_ptr(), T, q_out.data_ptr(), ldqo,
+                       k_out.data_ptr(), ldko, self._stream(stream))
+        if rc:
+            _check("eva_rope_run", rc)
+        return q_out, k_out
+
+    def close(self):
+        if self.handle is not None:
+            eva_rope_destroy(self.handle)
+            self.handle = None
+
+
+class KVCache(_OnDevice):
+    """A paged 8-bit cache of keys and values and the attention over it.
+
+    k, v: codes [num_pages][kv_heads][page_size][head_dim] (int8, or float8_e4m3fn), k_scale, v_scale: float32
+    [num_pages][kv_heads]; made here (zeros) when not given.  max_seqs and max_pages bound a call's sequences
+    and the page table's columns.  One handle must not attend on two streams at once; clone(), another handle over
+    the same buffers, may."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, *, num_pages, max_seqs, max_pages, page_size=64, dtype="int8",
+                 window=0, softcap=0.0, scale=None, out_dtype="float16", k=None, v=None, k_scale=None, v_scale=None,
+                 device=None, stream=None):
+        import torch
+        self.handle = None
+        if dtype not in ("int8", "e4m3"):
+            raise ValueError(f"dtype must be 'int8' or 'e4m3', not {dtype!r}")
+        if scale is not None and not scale > 0:
+            raise ValueError("scale must be positive")
+        self._args = dict(num_pages=num_pages, max_seqs=max_seqs, max_pages=max_pages, page_size=page_size, dtype=dtype,
+                          window=window, softcap=softcap, scale=scale, out_dtype=out_dtype)
+        self.q_heads, self.kv_heads, self.head_dim = int(q_heads), int(kv_heads), int(head_dim)
+        self.max_seqs, self.max_pages = int(max_seqs), int(max_pages)
+        self.out_dtype, code_out = _dtype(out_dtype)
+        given = [t for t in (k, v, k_scale, v_scale) if t is not None]
+        if device is None:
+            device = given[0].device if given else torch.device("cuda", torch.cuda.current_device())
+        self.device = torch.device("cuda", torch.device(device).index or 0)
+        code_type = torch.int8 if dtype == "int8" else torch.float8_e4m3fn
+        tile = (int(num_pages), self.kv_heads)
+        made = []
+        for name, t, shape, kind in (("k", k, tile + (int(page_size), self.head_dim), code_type),
+                                     ("v", v, tile + (int(page_size), self.head_dim), code_type),
+                                     ("k_scale", k_scale, tile, torch.float32), ("v_scale", v_scale, tile, torch.float32)):
+            if t is None:
+                t = torch.zeros(shape, dtype=kind, device=self.device)
+            elif t.dtype != kind or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {kind} tensor {shape} on {self.device}")
+            made.append(t)
+        self.k, self.v, self.k_scale, self.v_scale = made
+        self.desc = eva_kv_desc(self.q_heads, self.kv_heads, self.head_dim, int(page_size), int(num_pages), self.max_seqs,
+                                self.max_pages, EVA_CACHE_INT8 if dtype == "int8" else EVA_CACHE_E4M3, code_out,
+                                int(window), float(softcap), float(scale or 0.0))
+        with torch.cuda.device(self.device):
+            self.handle = eva_kv_create(self.desc, *map(_ptr, made), self._stream(stream))
+        lib = load()
+        self._append, self._attend, self._read = lib.eva_kv_append, lib.eva_kv_attend, lib.eva_kv_read
+
+    def clone(self, **changes):
+        """Another handle (its own workspace) over the same buffers; changes: window, softcap, scale, out_dtype,
+        max_seqs, max_pages."""
+        return KVCache(self.q_heads, self.kv_heads, self.head_dim, **{**self._args, **changes}, k=self.k, v=self.v,
+                       k_scale=self.k_scale, v_scale=self.v_scale)
+
+    def _sequences(self, starts, lens, page_table, what="lens"):
+        dev = self.device
+        B = lens.shape[0]
+        if not 1 <= B <= self.max_seqs:
+            raise ValueError(f"{B} sequences: 1 to {self.max_seqs} were planned for")
+        _indices(what, lens, (B,), dev)
+        _indices("starts", starts, (B + 1,), dev)
+        _indices("page_table", page_table, (B, self.max_pages), dev)
+        return B
+
+    def append(self, k, v, starts, lens, page_table, stream=None):
+        """Write the keys and values of new tokens: k, v [T][kv_heads][head_dim], fp16 or fp32 (rows may lie apart);
+        starts int32 [B + 1] (rows of each sequence), lens int32 [B] (lengths with them), page_table int32
+        [B][max_pages]."""
+        B = self._sequences(starts, lens, page_table)
+        dtype, code = _dtype(k.dtype)
+        T, ldk = _rows("k", k, self.kv_heads, self.head_dim, dtype, self.device)
+        Tv, ldv = _rows("v", v, self.kv_heads, self.head_dim, dtype, self.device)
+        if T != Tv:
+            raise ValueError(f"k has {T} rows, v has {Tv}")
+        rc = self._append(self.handle, k.data_ptr(), ldk, v.data_ptr(), ldv, code, starts.data_ptr(), lens.data_ptr(),
+                          page_table.data_ptr(), B, T, self._stream(stream))
+        if rc:
+            _check("eva_kv_append", rc)
+
+    def attend(self, q, starts, lens, page_table, out=None, lse=None, stream=None):
+        """Causal attention of q fp16 [T][q_heads][head_dim] over the cache -> [T][q_heads][head_dim].  Rows
+        behind starts[B] are not written: give `out` where they matter.  lse: optional float32 [T][q_heads]."""
+        import torch
+        B = self._sequences(starts, lens, page_table)
+        Hq, D, dev = self.q_heads, self.head_dim, self.device
+        T, ldq = _rows("q", q, Hq, D, torch.float16, dev)
+        if out is None:
+            out = self._empty((T, Hq, D), self.out_dtype, stream)
+        elif _rows("out", out, Hq, D, self.out_dtype, dev) != (T, Hq * D):
+            raise ValueError(f"out must be a contiguous [{T}][{Hq}][{D}] tensor")
+        if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != (T, Hq) or
+                                not lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous float32 tensor ({T}, {Hq}) on {dev}")
+        rc = self._attend(self.handle, q.data_ptr(), ldq, starts.data_ptr(), lens.data_ptr(), page_table.data_ptr(), B, T,
+                          out.data_ptr(), None if lse is None else lse.data_ptr(), self._stream(stream))
+        if rc:
+            _check("eva_kv_attend", rc)
+        return out
+
+    def read(self, starts, begins, page_table, rows, k_out=None, v_out=None, dtype="float16", stream=None):
+        """The stored values back: (k, v) [rows][kv_heads][head_dim], where rows starts[b] .. hold the tokens at
+        positions begins[b] .. of sequence b."""
+        B = self._sequences(starts, begins, page_table, "begins")
+        dtype, code = _dtype(dtype)
+        shape = (int(rows), self.kv_heads, self.head_dim)
+        outs = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is None:
+                t = self._empty(shape, dtype, stream)
+            elif t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}")
+            outs.append(t)
+        rc = self._read(self.handle, starts.data_ptr(), begins.data_ptr(), page_table.data_ptr(), B, shape[0], code,
+                        outs[0].data_ptr(), outs[1].data_ptr(), self._stream(stream))
+        if rc:
+            _check("eva_kv_read", rc)
+        return tuple(outs)
+
+    def status(self) -> int:
+        """Waits for the device; EVA_OK, EVA_ERR_BAD_INDEX or EVA_ERR_DEVICE_TIMEOUT since the last call of this."""
+        return eva_kv_sync_status(self.handle)
+
+    def info(self) -> eva_kv_info:
+        return eva_kv_cache_info(self.handle)
+
+    def close(self):
+        if self.handle is not None:
+            eva_kv_destroy(self.handle)
+            self.handle = None
