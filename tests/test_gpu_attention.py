@@ -248,6 +248,13 @@ ATTEND = [
     ("int8", 64, 8, 8, 128, [12, 9], [15, 12], 0, 0.0, "float16"),              # more rows than positions: zeros
     ("int8", 64, 1, 1, 128, [6000], [1], 0, 0.0, "float16"),                    # one item over many CTAs
     ("e4m3", 32, 8, 1, 128, [4001, 60], [1, 1], 1, 0.0, "float16"),             # a window of the row itself
+    # many steps and many items a CTA: the ring and the pieces come round many times
+    ("int8", 64, 8, 8, 128, [1400 - 21 * i for i in range(66)], [1] * 66, 0, 0.0, "float16"),
+    ("e4m3", 16, 32, 8, 64, [1 + 37 * i for i in range(50)], [1] * 50, 0, 0.0, "float16"),
+    ("int8", 32, 8, 4, 256, [2 + 90 * (i % 17) for i in range(35)], [1] * 35, 0, 0.0, "float16"),
+    ("int8", 64, 16, 4, 128, [3000, 2999, 1], [8, 5, 1], 0, 0.0, "float16"),
+    ("e4m3", 128, 32, 4, 64, [2500, 90, 2600], [40, 3, 33], 0, 0.0, "float16"),
+    ("int8", 16, 16, 8, 128, [60 + i for i in range(40)], [4] * 40, 0, 0.0, "float16"),
 ]
 
 

@@ -163,14 +163,15 @@ __device__ __forceinline__ long long at_seq_steps(const KvSeq &s, int rows, cons
 
 // A CTA's part of the line, walked item by item; uniform over a warp.
 struct AtWalk {
-    long long total, at, end;          // steps of the line, the next one, this part's end
+    long long total, at;               // steps of the line, the next one
+    int left;                          // steps of this part from there on
     int parts;                         // CTAs that take a part
     int b, rt, nrt, h;                 // the item
     KvSeq seq;
     AtTile tile;
     int off;                           // steps of the item that lie before `at`
 
-    __device__ __forceinline__ int piece() const { return (int)min((long long)(tile.n - off), end - at); }
+    __device__ __forceinline__ int piece() const { return min(tile.n - off, left); }
 
     __device__ __forceinline__ void init(const AttendParams &p, int rows, bool &bad) {
         const int lane = threadIdx.x & 31;
@@ -184,10 +185,10 @@ struct AtWalk {
         }
         parts = (int)min((long long)gridDim.x, (total + p.min_steps - 1) / p.min_steps);
         const int c = blockIdx.x;
-        at = end = 0;
+        left = 0;
         if (c >= parts) return;
         at = total * c / parts;
-        end = total * (c + 1) / parts;
+        left = (int)(total * (c + 1) / parts - at);
         long long before = 0;
         for (int b0 = 0; b0 < p.tok.B; b0 += 32) {
             long long w = 0;
@@ -209,20 +210,21 @@ struct AtWalk {
         }
         seq = kv_seq(p.tok, b, bad);
         nrt = at_tiles(seq, rows, p.G);
-        long long left = at - before;
+        long long in = at - before;
         for (rt = 0;; ++rt) {
             tile = at_tile(seq, rt, rows, p.G, p.window);
-            if (left < (long long)tile.n * p.H || rt + 1 >= nrt) break;
-            left -= (long long)tile.n * p.H;
+            if (in < (long long)tile.n * p.H || rt + 1 >= nrt) break;
+            in -= (long long)tile.n * p.H;
         }
-        h = (int)(left / tile.n);
-        off = (int)(left - (long long)h * tile.n);
+        h = (int)(in / tile.n);
+        off = (int)(in - (long long)h * tile.n);
     }
     // past the current piece of n steps
     __device__ __forceinline__ void next(const AttendParams &p, int rows, int n, bool &bad) {
         at += n;
+        left -= n;
         off = 0;
-        if (at >= end) return;
+        if (left <= 0) return;
         if (++h < p.H) return;
         h = 0;
         if (++rt >= nrt) {
@@ -244,8 +246,20 @@ struct AtWalk {
 // over it; factor < 0 marks tokens that are not there.
 struct AtScales {
     float sk[2], lsv[2], rsv[2];
-    float pad[2];
+    int tag, pad;                      // the step's number in its CTA
 };
+
+// One piece of the line, as the streaming warp hands it to the others (n 0: no more).
+struct AtPiece {
+    int n, s_first;                    // steps, and the first one's number in its sequence
+    int row, rows, len;                // first packed row and row count of the sequence, its length
+    int rt, h;
+    int whole, slot;                   // covers its item; else where its sums go
+    int c0, c1;                        // parts that share the item
+    int pad;
+};
+constexpr int kAtPieces = 4;           // handed over ahead
+constexpr int kAtSmemPerSm = 228 * 1024;
 
 template <int D, int NT, int WR, int WARPS>
 struct AtShape {
@@ -253,24 +267,31 @@ struct AtShape {
     static constexpr int kGroups = WARPS / WR;             // warps that take different steps
     static constexpr int kStepBytes = 2 * kAtStep * D;
     static constexpr int kThreads = 32 * (WARPS + 1);
-    static constexpr bool kQShared = NT > 1;               // queries in shared memory (else registers)
+    // Resident CTAs an SM, by registers: warps are dealt to four schedulers of 16384 registers each, so 16 warps
+    // get 128 each, 12 get 168, 8 get 255.
+    static constexpr int kCtas = NT * D <= 128 ? (WARPS < 6 ? 3 : 2) : NT * D <= 256 && WARPS < 6 ? 2 : 1;
     static constexpr int kQStride = D + 16;                // halves; 8 g + 2 c words: no conflicts
     static constexpr int kOStride = D + 4;                 // floats; 8 c + 2 g words: no conflicts
-    static constexpr size_t kQBytes = kQShared ? (size_t)kRows * kQStride * 2 : 0;
+    static constexpr size_t kQBytes = (size_t)kRows * kQStride * 2;
     static constexpr size_t kOBytes = (size_t)kGroups * kRows * kOStride * 4;
     static constexpr size_t kMlBytes = (size_t)kGroups * kRows * 8;
-    static size_t smem(int stages) {
-        return 1024 + (size_t)stages * (kStepBytes + sizeof(AtScales) + 16) + kQBytes + kOBytes + kMlBytes + kRows * 4 + 64;
-    }
+    static constexpr size_t kStageBytes = kStepBytes + sizeof(AtScales) + 16;
+    static constexpr size_t kFixedBytes = 1024 + kQBytes + kOBytes + kMlBytes + kAtPieces * (sizeof(AtPiece) + 16) + 64;
+    // the ring takes what a CTA's share of the 228 KB leaves (1 KB a CTA is the system's)
+    static constexpr int kRoom = (int)((kAtSmemPerSm / kCtas - 1024 - kFixedBytes) / kStageBytes);
+    static constexpr int kStages = kRoom < 16 ? kRoom : 16;
+    static constexpr bool kTagged = kStages % kGroups != 0;
+    static constexpr size_t kSmem = kFixedBytes + kStages * kStageBytes;
+    static_assert(kStages >= kGroups, "each warp needs a stage of its own");
 };
 
 template <int D, int NT, int WR, int WARPS, bool E4M3>
-__global__ void __launch_bounds__(32 * (WARPS + 1))
-    eva_attend_kernel(const __grid_constant__ AttendMaps maps, AttendParams p, int stages) {
+__global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::kCtas)
+    eva_attend_kernel(const __grid_constant__ AttendMaps maps, AttendParams p) {
     using S = AtShape<D, NT, WR, WARPS>;
-    constexpr int kRows = S::kRows, kGroups = S::kGroups, kChunks = D / 16;
+    constexpr int kRows = S::kRows, kGroups = S::kGroups, kChunks = D / 16, stages = S::kStages;
     constexpr int kBarConsumers = 1;
-    // shared memory: ring | scales | full and free barriers | queries | outputs | statistics
+    // shared memory: ring | scales | full and free barriers | pieces and theirs | queries | outputs | statistics
     const uint32_t base0 = (uint32_t)__cvta_generic_to_shared(eva_smem);
     const uint32_t skip = ((base0 + 1023) & ~1023u) - base0;
     uint8_t *ring = eva_smem + skip;
@@ -278,7 +299,10 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
     AtScales *scales = reinterpret_cast<AtScales *>(ring + (size_t)stages * S::kStepBytes);
     uint64_t *bars = reinterpret_cast<uint64_t *>(scales + stages);
     const uint32_t full_a = (uint32_t)__cvta_generic_to_shared(bars), free_a = full_a + 8 * stages;
-    __half *qs = reinterpret_cast<__half *>(bars + 2 * stages);
+    uint64_t *pbars = bars + 2 * stages;
+    const uint32_t pfull_a = free_a + 8 * stages, pfree_a = pfull_a + 8 * kAtPieces;
+    AtPiece *pieces = reinterpret_cast<AtPiece *>(pbars + 2 * kAtPieces);
+    __half *qs = reinterpret_cast<__half *>(pieces + kAtPieces);
     float *os = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(qs) + S::kQBytes);
     float2 *mls = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(os) + S::kOBytes);
     // [0] this CTA joins the item, [1] a warp of this CTA gave up a wait
@@ -287,96 +311,149 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
+            scales[i].tag = -1;
             mbar_init(full_a + 8 * i, 1);
             mbar_init(free_a + 8 * i, WR);
+        }
+        for (int i = 0; i < kAtPieces; ++i) {
+            mbar_init(pfull_a + 8 * i, 1);
+            mbar_init(pfree_a + 8 * i, WARPS);
         }
         flag[1] = 0;
     }
     __syncthreads();
     pdl_wait();
     pdl_launch();
-    bool bad = false;
-    AtWalk walk;
-    walk.init(p, kRows, bad);
 
     if (warp == WARPS) {
         // ------------------------------------------------ the streaming warp
+        bool bad = false;
+        AtWalk walk;
+        walk.init(p, kRows, bad);
+        int ps = 0;                    // piece slot
+        uint32_t pparity = 1;
+        auto hand = [&](int n) {
+            if (!mbar_wait_bounded(pfree_a + 8 * ps, pparity, p.wait_rounds)) return false;
+            if (lane == 0) {
+                AtPiece &q = pieces[ps];
+                q.n = n;
+                if (n > 0) {
+                    const long long lo = walk.at - walk.off;             // the item's first step of the line
+                    q.s_first = walk.tile.s0 + walk.off;
+                    q.row = walk.seq.row;
+                    q.rows = walk.seq.n;
+                    q.len = walk.seq.len;
+                    q.rt = walk.rt;
+                    q.h = walk.h;
+                    q.whole = n == walk.tile.n;
+                    q.slot = 2 * blockIdx.x + (walk.off > 0 ? 0 : 1);
+                    q.c0 = q.whole ? 0 : walk.part_of(lo);
+                    q.c1 = q.whole ? 0 : walk.part_of(lo + walk.tile.n - 1);
+                }
+                mbar_arrive(pfull_a + 8 * ps);
+            }
+            __syncwarp();
+            if (++ps == kAtPieces) {
+                ps = 0;
+                pparity ^= 1;
+            }
+            return true;
+        };
+        // Each lane looks up the pages and scales of one step of the next 32 and issues that step's copies itself, so
+        // a step costs the warp one wait and a few instructions; the following 32 steps' lookups are in flight
+        // meanwhile.
         const int page = p.tok.page, boxes = page < kAtStep ? 2 : 1;     // boxes of a step
         const int box_rows = kAtStep / boxes;
-        int t = 0;
-        bool ok = !p.inject;
-        while (walk.at < walk.end && ok) {
+        int st = 0, t = 0;
+        uint32_t parity = 1;           // of the free barriers: the first round passes at once
+        bool ok = true;
+        while (walk.left > 0 && ok) {
             const int n = walk.piece(), s_first = walk.tile.s0 + walk.off;
-            const long long row = (long long)walk.b * p.tok.max_pages;
-            for (int s0 = 0; s0 < n && ok; s0 += 32) {
-                // each lane looks up one step: its pages (-1: no token there) and their scales
-                int pid[2] = {-1, -1};
-                float sk[2] = {-1.f, -1.f}, sv[2] = {1.f, 1.f};
-                if (s0 + lane < n) {
-                    const int tok0 = (s_first + s0 + lane) * kAtStep;
+            ok = hand(n) && !p.inject;
+            const int32_t *table = p.tok.table + (long long)walk.b * p.tok.max_pages;
+            int pid[2], pid_next[2];   // page of each half of this lane's step, -1: no token there
+            float sk[2], sv[2], sk_next[2], sv_next[2];
+            auto look = [&](int s, int (&id)[2]) {
+                id[0] = id[1] = -1;
+                if (s >= n) return;
+                const int tok0 = (s_first + s) * kAtStep;
+                if (tok0 < walk.seq.len) id[0] = table[tok0 / page];
+                if (tok0 + 16 < walk.seq.len) id[1] = boxes == 1 ? id[0] : table[tok0 / page + 1];
+            };
+            auto scale = [&](int s, int (&id)[2], float (&k)[2], float (&v)[2]) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (i == 1 && boxes == 1) {
-                            if (tok0 + 16 < walk.seq.len) pid[1] = pid[0];
-                        } else if (tok0 + 16 * i < walk.seq.len) {
-                            pid[i] = p.tok.table[row + (tok0 + 16 * i) / page];
-                            if (pid[i] < 0 || pid[i] >= p.tok.num_pages) {
-                                bad = true;
-                                pid[i] = -1;
-                            }
-                        }
+                for (int i = 0; i < 2; ++i) {
+                    if (id[i] < 0 || id[i] >= p.tok.num_pages) {
+                        if (s < n && (s_first + s) * kAtStep + 16 * i < walk.seq.len) bad = true;
+                        id[i] = -1;
                     }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (pid[i] < 0) continue;
-                        sk[i] = p.k_scale[(long long)pid[i] * p.H + walk.h];
-                        sv[i] = p.v_scale[(long long)pid[i] * p.H + walk.h];
-                    }
+                    const bool there = id[i] >= 0;
+                    k[i] = there ? p.k_scale[(long long)id[i] * p.H + walk.h] : -1.f;
+                    v[i] = there ? p.v_scale[(long long)id[i] * p.H + walk.h] : 1.f;
                 }
+            };
+            look(lane, pid);
+            scale(lane, pid, sk, sv);
+            for (int s0 = 0; s0 < n && ok; s0 += 32) {
+                look(s0 + 32 + lane, pid_next);
+                AtScales sc = {};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float e = fmaxf(sv[i] * AtCode<E4M3>::kUnit, 1e-30f);
+                    sc.sk[i] = pid[i] < 0 ? -1.f : sk[i] * AtCode<E4M3>::kUnit;
+                    sc.lsv[i] = log2f(e);
+                    sc.rsv[i] = 1.f / e;
+                }
+                const int slot = (s_first + s0 + lane) * kAtStep & (page - 1);
+                const int y0 = (pid[0] * p.H + walk.h) * page + (boxes == 2 ? 0 : slot), y1 = (pid[1] * p.H + walk.h) * page;
+                const bool two = boxes == 2 && pid[1] >= 0;
+                const uint32_t bytes = (uint32_t)(((pid[0] >= 0) + two) * 2 * box_rows * D);
                 const int steps = min(32, n - s0);
-                for (int i = 0; i < steps; ++i, ++t) {
-                    const int st = t % stages, round = t / stages;
-                    if (round > 0 && !mbar_wait_bounded(free_a + 8 * st, (round - 1) & 1, p.wait_rounds)) {
+                for (int i = 0; i < steps; ++i) {
+                    if (!mbar_wait_bounded(free_a + 8 * st, parity, p.wait_rounds)) {
                         ok = false;
                         break;
                     }
-                    const int p0 = __shfl_sync(0xffffffffu, pid[0], i), p1 = __shfl_sync(0xffffffffu, pid[1], i);
-                    const float k0 = __shfl_sync(0xffffffffu, sk[0], i), k1 = __shfl_sync(0xffffffffu, sk[1], i);
-                    const float v0 = __shfl_sync(0xffffffffu, sv[0], i), v1 = __shfl_sync(0xffffffffu, sv[1], i);
-                    if (lane == 0) {
+                    if (lane == i) {
                         const uint32_t bar = full_a + 8 * st, dst = ring_a + st * S::kStepBytes;
-                        const int live = (p0 >= 0) + (boxes == 2 && p1 >= 0);
-                        AtScales &sc = scales[st];
-                        const float e0 = fmaxf(v0 * AtCode<E4M3>::kUnit, 1e-30f), e1 = fmaxf(v1 * AtCode<E4M3>::kUnit, 1e-30f);
-                        sc.sk[0] = p0 < 0 ? -1.f : k0 * AtCode<E4M3>::kUnit;
-                        sc.sk[1] = p1 < 0 ? -1.f : k1 * AtCode<E4M3>::kUnit;
-                        sc.lsv[0] = log2f(e0);
-                        sc.lsv[1] = log2f(e1);
-                        sc.rsv[0] = 1.f / e0;
-                        sc.rsv[1] = 1.f / e1;
-                        if (live)
-                            mbar_arrive_expect_tx(bar, (uint32_t)(live * 2 * box_rows * D));
+                        sc.tag = t;
+                        scales[st] = sc;
+                        if (bytes)
+                            mbar_arrive_expect_tx(bar, bytes);
                         else
                             mbar_arrive(bar);
-                        const int slot = (s_first + s0 + i) * kAtStep % page;
 #pragma unroll
-                        for (int bx = 0; bx < 2; ++bx) {
-                            const int id = bx ? p1 : p0;
-                            if (bx >= boxes || id < 0) continue;
-                            const int y = (id * p.H + walk.h) * page + (boxes == 2 ? 0 : slot);
-#pragma unroll
-                            for (int x = 0; x < D; x += 128) {     // a column half of 128 bytes is [32][128]
-                                const uint32_t o = dst + (uint32_t)(x * kAtStep + bx * box_rows * (D < 128 ? D : 128));
-                                at_tma_2d(o, &maps.k, x, y, bar);
-                                at_tma_2d(o + kAtStep * D, &maps.v, x, y, bar);
+                        for (int x = 0; x < D; x += 128) {     // a column half of 128 bytes is [32][128]
+                            const uint32_t o = dst + (uint32_t)(x * kAtStep);
+                            if (pid[0] >= 0) {
+                                at_tma_2d(o, &maps.k, x, y0, bar);
+                                at_tma_2d(o + kAtStep * D, &maps.v, x, y0, bar);
+                            }
+                            if (two) {
+                                const uint32_t o2 = o + (uint32_t)(16 * (D < 128 ? D : 128));
+                                at_tma_2d(o2, &maps.k, x, y1, bar);
+                                at_tma_2d(o2 + kAtStep * D, &maps.v, x, y1, bar);
                             }
                         }
                     }
                     __syncwarp();
+                    if (++st == stages) {
+                        st = 0;
+                        parity ^= 1;
+                    }
+                    ++t;
+                    if (i == 8) scale(s0 + 32 + lane, pid_next, sk_next, sv_next);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    pid[i] = pid_next[i];
+                    sk[i] = sk_next[i];
+                    sv[i] = sv_next[i];
                 }
             }
             walk.next(p, kRows, n, bad);
         }
+        if (ok) ok = hand(0);
         if (bad) atomicOr(p.status, kKvStatusIndex);
         if (!ok) {                     // a consumer gave up: record it, let the copies in flight land
             if (lane == 0) atomicOr(p.status, kAtStatusWait);
@@ -392,37 +469,35 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
     constexpr float kLog2e = 1.4426950408889634f;
     const float zscale = p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e;
     const float zcap = p.cap * kLog2e;
-    int t0 = 0;
-    bool ok = true;
-    while (walk.at < walk.end && ok) {
-        const int n = walk.piece(), s_first = walk.tile.s0 + walk.off;
-        const KvSeq seq = walk.seq;
-        const int r0 = walk.rt * kRows, nrows = min(kRows, seq.n * p.G - r0);
+    int t0 = 0;                        // steps of earlier pieces: step t of this CTA is group t % kGroups's
+    int own = grp;                     // stage of this warp's next step, and its parity (stages >= kGroups)
+    uint32_t own_parity = 0;
+    int ps = 0;
+    uint32_t pparity = 0;
+    for (;;) {
+        const bool got = mbar_wait_bounded(pfull_a + 8 * ps, pparity, p.wait_rounds);
+        if (!got && lane == 0) flag[1] = 1;
+        const AtPiece &pc = pieces[ps];
+        const int n = got ? pc.n : 0, s_first = pc.s_first;
+        const KvSeq seq = {pc.row, pc.rows, pc.len};
+        const int r0 = pc.rt * kRows, nrows = min(kRows, seq.n * p.G - r0), h = pc.h;
         // queries
-        uint32_t qf[S::kQShared ? 1 : kChunks][2];
         auto qrow = [&](int r) {       // r: row of the item
-            const int i = (r0 + r) / p.G, hq = walk.h * p.G + (r0 + r) - i * p.G;
+            const int i = (r0 + r) / p.G, hq = h * p.G + (r0 + r) - i * p.G;
             return p.q + (seq.row + i) * p.ldq + (long long)hq * D;
         };
-        if constexpr (S::kQShared) {
+        if (n > 0) {
+#pragma unroll 1
             for (int i = tid; i < kRows * (D / 8); i += 32 * WARPS) {
                 const int r = i / (D / 8), x = i - r * (D / 8);
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (r < nrows) v = reinterpret_cast<const uint4 *>(qrow(r))[x];
                 *reinterpret_cast<uint4 *>(qs + r * S::kQStride + x * 8) = v;
             }
-            asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
-        } else {
-            const bool live = wr * 8 + g < nrows;
-            const __half *src = live ? qrow(wr * 8 + g) : nullptr;
-#pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) {
-                uint2 v = make_uint2(0, 0);
-                if (live) v = *reinterpret_cast<const uint2 *>(src + ch * 16 + 4 * c);
-                qf[ch][0] = v.x;
-                qf[ch][1] = v.y;
-            }
         }
+        // all warps leave together: at the last piece, or when one has given up a wait
+        asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
+        if (n == 0 || flag[1]) break;
         // positions: the last key each of this lane's rows sees
         int last[NT][2];
 #pragma unroll
@@ -445,10 +520,24 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
         }
 
         for (int i = ((grp - t0) % kGroups + kGroups) % kGroups; i < n; i += kGroups) {
-            const int t = t0 + i, st = t % stages;
-            if (!mbar_wait_bounded(full_a + 8 * st, (t / stages) & 1, p.wait_rounds)) {
+            const int st = own;
+            bool there = true;
+            if constexpr (S::kTagged) {
+                // Where a stage passes from warp to warp, a warp may be two rounds behind, and a barrier's parity
+                // would tell it that its step is there.  Once the stage carries this step's number, every earlier
+                // round is over and the parity is unambiguous.
+                int tries = 0;
+                while (*reinterpret_cast<volatile int *>(&scales[st].tag) != t0 + i && ++tries < p.wait_rounds) __nanosleep(20);
+                there = tries < p.wait_rounds;
+            }
+            if (!there || !mbar_wait_bounded(full_a + 8 * st, own_parity, p.wait_rounds)) {
                 if (lane == 0) flag[1] = 1;
                 break;
+            }
+            own += kGroups;
+            if (own >= stages) {
+                own -= stages;
+                own_parity ^= 1;
             }
             const uint32_t kt = ring_a + st * S::kStepBytes, vt = kt + kAtStep * D;
             const AtScales sc = scales[st];
@@ -482,18 +571,10 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        uint32_t b0, b1;
-                        if constexpr (S::kQShared) {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(
-                                qs + ((wr * NT + nt) * 8 + g) * S::kQStride + (ch + x) * 16 + 4 * c);
-                            b0 = v.x;
-                            b1 = v.y;
-                        } else {
-                            b0 = qf[ch + x][0];
-                            b1 = qf[ch + x][1];
-                        }
-                        at_mma(z[nt][0], a[0][x], b0, b1);
-                        at_mma(z[nt][1], a[1][x], b0, b1);
+                        const uint2 v = *reinterpret_cast<const uint2 *>(
+                            qs + ((wr * NT + nt) * 8 + g) * S::kQStride + (ch + x) * 16 + 4 * c);
+                        at_mma(z[nt][0], a[0][x], v.x, v.y);
+                        at_mma(z[nt][1], a[1][x], v.x, v.y);
                     }
                 }
             }
@@ -588,14 +669,14 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
                     *reinterpret_cast<float2 *>(dst + ch * 16) = make_float2(o[nt][ch][e], o[nt][ch][e + 2]);
             }
         asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
-        ok = flag[1] == 0;             // the same answer in every warp: nothing sets it before the barrier below
-        const bool whole = n == walk.tile.n;
-        const long long lo = walk.at - walk.off;             // the item's first step of the line
-        const int slot = walk.off > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1;
+        // read again rather than held in registers through the steps
+        const int e0 = pc.rt * kRows, erows = min(kRows, pc.rows * p.G - e0), eh = pc.h, erow = pc.row;
+        const bool whole = pc.whole;
+        const int slot = pc.slot;
         auto emit = [&](int r, int x, const float4 &v, float mm, float ll) {
-            const int i = (r0 + r) / p.G, hq = walk.h * p.G + (r0 + r) - i * p.G;
+            const int i = (e0 + r) / p.G, hq = eh * p.G + (e0 + r) - i * p.G;
             const float f = ll > 0.f ? 1.f / ll : 0.f;
-            const long long at = ((long long)(seq.row + i) * p.Hq + hq) * D + x;
+            const long long at = ((long long)(erow + i) * p.Hq + hq) * D + x;
             if (p.out_f32) {
                 *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
                     make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
@@ -605,9 +686,10 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
                     make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
             }
             if (p.lse && x == 0)
-                p.lse[(long long)(seq.row + i) * p.Hq + hq] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                p.lse[(long long)(erow + i) * p.Hq + hq] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
         };
-        for (int i = tid; i < nrows * (D / 4); i += 32 * WARPS) {
+#pragma unroll 1
+        for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
             const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
             float mm = -INFINITY;
 #pragma unroll
@@ -632,7 +714,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
         }
         if (!whole) {
             // the last part of the item to finish joins them all
-            const int c0 = walk.part_of(lo), c1 = walk.part_of(lo + walk.tile.n - 1);
+            const int c0 = pc.c0, c1 = pc.c1;
             __threadfence();
             asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
             if (tid == 0) {
@@ -643,7 +725,8 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
             }
             asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
             if (flag[0]) {
-                for (int i = tid; i < nrows * (D / 4); i += 32 * WARPS) {
+#pragma unroll 1
+                for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
                     const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
                     float mm = -INFINITY;
                     for (int cc = c0; cc <= c1; ++cc)
@@ -665,9 +748,13 @@ __global__ void __launch_bounds__(32 * (WARPS + 1))
         }
         asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
         t0 += n;
-        walk.next(p, kRows, n, bad);
+        if (lane == 0) mbar_arrive(pfree_a + 8 * ps);
+        if (++ps == kAtPieces) {
+            ps = 0;
+            pparity ^= 1;
+        }
     }
-    if (!ok && lane == 0) atomicOr(p.status, kAtStatusWait);
+    if (flag[1] && tid == 0) atomicOr(p.status, kAtStatusWait);
 }
 
 }  // namespace eva

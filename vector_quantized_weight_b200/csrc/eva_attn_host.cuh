@@ -151,28 +151,21 @@ eva_status_t validate_kv(const eva_kv_desc *d) {
     return EVA_OK;
 }
 
-using AttendFn = void (*)(const AttendMaps, AttendParams, int);
+using AttendFn = void (*)(const AttendMaps, AttendParams);
 
-// One attention instance: how deep its ring is and how many CTAs an SM holds.
-// Two CTAs an SM, so that one streams while the other joins or starts an item.
+// One attention instance: its shared memory and the CTAs the GPU holds at once.
 template <int D, int NT, int WR, int WARPS, bool E4M3>
-cudaError_t plan_attend(eva_kv *h, int i, int smem_per_sm, int optin) {
+cudaError_t plan_attend(eva_kv *h, int i, int optin) {
     using S = AtShape<D, NT, WR, WARPS>;
     auto fn = eva_attend_kernel<D, NT, WR, WARPS, E4M3>;
     eva_kv::Plan &p = h->plan[i];
     p.fn = reinterpret_cast<const void *>(fn);
     p.rows = S::kRows;
     p.threads = S::kThreads;
-    cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, fn);
-    if (e != cudaSuccess) return e;
-    const int by_regs = 65536 / ((attr.numRegs + 7) / 8 * 8 * S::kThreads);
-    const int want = std::max(1, std::min(2, by_regs));
-    const size_t room = std::min((size_t)optin, (size_t)smem_per_sm / want - 1024);
-    p.stages = 16;
-    while (p.stages > 2 && S::smem(p.stages) > room) --p.stages;
-    p.smem = S::smem(p.stages);
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+    p.stages = S::kStages;
+    p.smem = S::kSmem;
+    if (p.smem > (size_t)optin) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, S::kThreads, p.smem);
@@ -182,24 +175,26 @@ cudaError_t plan_attend(eva_kv *h, int i, int smem_per_sm, int optin) {
     return cudaSuccess;
 }
 template <int D, bool E4M3>
-cudaError_t plan_attends(eva_kv *h, int smem_per_sm, int optin) {
-    cudaError_t e = plan_attend<D, 1, 1, 4, E4M3>(h, 0, smem_per_sm, optin);
+cudaError_t plan_attends(eva_kv *h, int optin) {
     if constexpr (D <= 128) {
-        if (e == cudaSuccess) e = plan_attend<D, 2, 1, 4, E4M3>(h, 1, smem_per_sm, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 4, 1, 4, E4M3>(h, 2, smem_per_sm, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 4, 4, 4, E4M3>(h, 3, smem_per_sm, optin);
+        cudaError_t e = plan_attend<D, 1, 1, 4, E4M3>(h, 0, optin);
+        if (e == cudaSuccess) e = plan_attend<D, 2, 1, 4, E4M3>(h, 1, optin);
+        if (e == cudaSuccess) e = plan_attend<D, 4, 1, 7, E4M3>(h, 2, optin);
+        if (e == cudaSuccess) e = plan_attend<D, 4, 7, 7, E4M3>(h, 3, optin);
+        return e;
     } else {                             // 16 rows a warp would not fit in its registers
-        if (e == cudaSuccess) e = plan_attend<D, 1, 4, 4, E4M3>(h, 3, smem_per_sm, optin);
+        cudaError_t e = plan_attend<D, 1, 1, 7, E4M3>(h, 0, optin);
+        if (e == cudaSuccess) e = plan_attend<D, 1, 7, 7, E4M3>(h, 3, optin);
+        return e;
     }
-    return e;
 }
-cudaError_t plan_attends(eva_kv *h, int smem_per_sm, int optin) {
+cudaError_t plan_attends(eva_kv *h, int optin) {
     const bool e4 = h->desc.cache_dtype == EVA_CACHE_E4M3;
     switch (h->desc.head_dim) {
-        case 64: return e4 ? plan_attends<64, true>(h, smem_per_sm, optin) : plan_attends<64, false>(h, smem_per_sm, optin);
-        case 128: return e4 ? plan_attends<128, true>(h, smem_per_sm, optin) : plan_attends<128, false>(h, smem_per_sm, optin);
+        case 64: return e4 ? plan_attends<64, true>(h, optin) : plan_attends<64, false>(h, optin);
+        case 128: return e4 ? plan_attends<128, true>(h, optin) : plan_attends<128, false>(h, optin);
     }
-    return e4 ? plan_attends<256, true>(h, smem_per_sm, optin) : plan_attends<256, false>(h, smem_per_sm, optin);
+    return e4 ? plan_attends<256, true>(h, optin) : plan_attends<256, false>(h, optin);
 }
 
 // The cache as rows of head_dim bytes; a box is 16 or 32 tokens of at most 128 bytes.
@@ -382,7 +377,7 @@ eva_status_t eva_kv_create(eva_kv_t *out, const eva_kv_desc *desc, void *k_pages
         free_kv(h);
         return st;
     }
-    cudaError_t e = plan_attends(h, (int)prop.sharedMemPerMultiprocessor, (int)prop.sharedMemPerBlockOptin);
+    cudaError_t e = plan_attends(h, (int)prop.sharedMemPerBlockOptin);
     size_t slots = 0;
     for (const auto &p : h->plan) {
         slots = std::max(slots, (size_t)2 * p.grid * p.rows);
@@ -500,7 +495,7 @@ eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t
     h->last_plan = i;
     const eva_kv::Plan &pl = h->plan[i];
     return cuda_status(launch_pdl(reinterpret_cast<AttendFn>(const_cast<void *>(pl.fn)), dim3(pl.grid), dim3(pl.threads),
-                                  pl.smem, reinterpret_cast<cudaStream_t>(stream), 0, h->maps, p, pl.stages));
+                                  pl.smem, reinterpret_cast<cudaStream_t>(stream), 0, h->maps, p));
 }
 
 eva_status_t eva_kv_sync_status(eva_kv_t h) {
