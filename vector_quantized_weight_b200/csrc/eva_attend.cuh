@@ -28,10 +28,8 @@
 //    ldmatrix patterns are free of bank conflicts).  A page id outside the
 //    cache is never used as an address: its tokens count as masked and the
 //    status word is set.
-//  - Work is cut on the device, because only the device knows the lengths: the
-//    steps of all (sequence, row tile, key head) items form one line, and each
-//    CTA takes an equal part of it, whatever the items' borders.  An item that
-//    several CTAs share is joined by the last of them to finish, in the order
+//  - Work is cut on the device, because only the device knows the lengths
+//    (AtWalk).  An item (sequence, row tile, key head) that several CTAs share is joined by the last of them to finish, in the order
 //    of the parts, so results do not depend on timing.
 #pragma once
 #include <cuda.h>
@@ -155,76 +153,141 @@ __device__ __forceinline__ AtTile at_tile(const KvSeq &s, int rt, int rows, int 
     return t;
 }
 __device__ __forceinline__ int at_tiles(const KvSeq &s, int rows, int G) { return (s.n * G + rows - 1) / rows; }
-__device__ __forceinline__ long long at_seq_steps(const KvSeq &s, int rows, const AttendParams &p) {
-    long long w = 0;
-    for (int rt = 0, n = at_tiles(s, rows, p.G); rt < n; ++rt) w += at_tile(s, rt, rows, p.G, p.window).n;
-    return w * p.H;
-}
 
-// A CTA's part of the line, walked item by item; uniform over a warp.
+// A CTA's share of the work, walked piece by piece; uniform over a warp.
+//
+// Few items (at most half as many as CTAs): each is cut into equal parts of at
+// most S steps, S the smallest for which the parts are no more than the CTAs
+// (and at least min_steps: joining costs more than that many steps).  A CTA
+// has one piece.
+// Many items: they form one line, in which an item takes kAtItemCost steps
+// besides its own (starting and finishing it costs a CTA about that), and
+// every CTA takes an equal stretch, whatever the items' borders.
+constexpr int kAtItemCost = 4;
 struct AtWalk {
-    long long total, at;               // steps of the line, the next one
-    int left;                          // steps of this part from there on
-    int parts;                         // CTAs that take a part
+    long long total, at;               // the line's length, the current item's place in it
+    int left;                          // of this CTA's stretch from the current place on (few items: 1 or 0)
+    int parts;                         // CTAs that take a stretch (0: few items)
     int b, rt, nrt, h;                 // the item
     KvSeq seq;
     AtTile tile;
-    int off;                           // steps of the item that lie before `at`
+    int off;                           // of the item that lies before this CTA's stretch; few items: which part of
+    int k;                             // how many
 
-    __device__ __forceinline__ int piece() const { return min(tile.n - off, left); }
+    static __device__ __forceinline__ int cuts(int n, int S) { return (n + S - 1) / S; }
 
     __device__ __forceinline__ void init(const AttendParams &p, int rows, bool &bad) {
         const int lane = threadIdx.x & 31;
-        total = 0;
+        KvSeq first = {0, 0, 0};       // of the first 32 sequences, not loaded again
+        auto seq_of = [&](int b0) {
+            KvSeq s = first;
+            if (b0 > 0) {
+                s.n = 0;
+                if (b0 + lane < p.tok.B) s = kv_seq(p.tok, b0 + lane, bad);
+            }
+            return s;
+        };
+        if (lane < p.tok.B) first = kv_seq(p.tok, lane, bad);
+        long long steps = 0, items = 0;
         for (int b0 = 0; b0 < p.tok.B; b0 += 32) {
-            long long w = 0;
-            if (b0 + lane < p.tok.B) w = at_seq_steps(kv_seq(p.tok, b0 + lane, bad), rows, p);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-            total += w;
+            const KvSeq s = seq_of(b0);
+            const int n = at_tiles(s, rows, p.G);
+            for (int t = 0; t < n; ++t) steps += at_tile(s, t, rows, p.G, p.window).n;
+            items += n;
         }
-        parts = (int)min((long long)gridDim.x, (total + p.min_steps - 1) / p.min_steps);
-        const int c = blockIdx.x;
-        left = 0;
-        if (c >= parts) return;
-        at = total * c / parts;
-        left = (int)(total * (c + 1) / parts - at);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            steps += __shfl_xor_sync(0xffffffffu, steps, o);
+            items += __shfl_xor_sync(0xffffffffu, items, o);
+        }
+        steps *= p.H;
+        items *= p.H;
+        const int c = blockIdx.x, grid = gridDim.x;
+        const bool few = items * 2 <= grid;
+        int S = 0;
+        left = parts = 0;
+        at = total = 0;
+        if (items == 0) return;
+        long long place;               // this CTA's first part, or first step of the line
+        if (few) {
+            S = (int)max((long long)p.min_steps, (steps + grid - items - 1) / (grid - items));
+            place = c;
+        } else {
+            total = steps + items * kAtItemCost;
+            parts = (int)min((long long)grid, (total + p.min_steps - 1) / p.min_steps);
+            if (c >= parts) return;
+            place = total * c / parts;
+            left = (int)(total * (c + 1) / parts - place);
+        }
+        // the sequence, the row tile and the head that hold `place`
         long long before = 0;
-        for (int b0 = 0; b0 < p.tok.B; b0 += 32) {
+        unsigned who = 0;
+        for (int b0 = 0; b0 < p.tok.B && !who; b0 += 32) {
+            const KvSeq s = seq_of(b0);
             long long w = 0;
-            if (b0 + lane < p.tok.B) w = at_seq_steps(kv_seq(p.tok, b0 + lane, bad), rows, p);
+            for (int t = 0, n = at_tiles(s, rows, p.G); t < n; ++t) {
+                const int m = at_tile(s, t, rows, p.G, p.window).n;
+                w += few ? cuts(m, S) : m + kAtItemCost;
+            }
+            w *= p.H;
             long long sum = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long v = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += v;
             }
-            const unsigned who = __ballot_sync(0xffffffffu, at >= before + sum - w && at < before + sum);
-            if (who) {
-                const int src = __ffs(who) - 1;
-                b = b0 + src;
-                before += __shfl_sync(0xffffffffu, sum - w, src);
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, sum, 31);
+            who = __ballot_sync(0xffffffffu, place >= before + sum - w && place < before + sum);
+            const int src = who ? __ffs(who) - 1 : 31;
+            b = b0 + src;
+            before += __shfl_sync(0xffffffffu, who ? sum - w : sum, src);
+            seq.row = __shfl_sync(0xffffffffu, s.row, src);
+            seq.n = __shfl_sync(0xffffffffu, s.n, src);
+            seq.len = __shfl_sync(0xffffffffu, s.len, src);
         }
-        seq = kv_seq(p.tok, b, bad);
+        if (!who) {                    // few items, and fewer parts than CTAs
+            left = 0;
+            return;
+        }
         nrt = at_tiles(seq, rows, p.G);
-        long long in = at - before;
+        long long in = place - before;
+        int w = 1;
         for (rt = 0;; ++rt) {
             tile = at_tile(seq, rt, rows, p.G, p.window);
-            if (in < (long long)tile.n * p.H || rt + 1 >= nrt) break;
-            in -= (long long)tile.n * p.H;
+            w = few ? cuts(tile.n, S) : tile.n + kAtItemCost;
+            if (in < (long long)w * p.H || rt + 1 >= nrt) break;
+            in -= (long long)w * p.H;
         }
-        h = (int)(in / tile.n);
-        off = (int)(in - (long long)h * tile.n);
+        h = (int)(in / w);
+        off = (int)(in - (long long)h * w);
+        k = w;
+        at = place - off;
+        if (few) left = 1;
     }
-    // past the current piece of n steps
-    __device__ __forceinline__ void next(const AttendParams &p, int rows, int n, bool &bad) {
-        at += n;
-        left -= n;
-        off = 0;
+
+    // This CTA's steps [lo, hi) of the current item (none: the stretch holds only some of its extra), and the CTAs
+    // c0 .. c1 that share the item.
+    __device__ __forceinline__ void piece(int &lo, int &hi, int &c0, int &c1) const {
+        if (parts == 0) {
+            lo = (int)((long long)tile.n * off / k);
+            hi = (int)((long long)tile.n * (off + 1) / k);
+            c0 = blockIdx.x - off;
+            c1 = c0 + k - 1;
+        } else {
+            lo = max(0, off - kAtItemCost);
+            hi = min(tile.n, off + left - kAtItemCost);
+            c0 = part_of(at + kAtItemCost);
+            c1 = part_of(at + kAtItemCost + tile.n - 1);
+        }
+    }
+    __device__ __forceinline__ void next(const AttendParams &p, int rows, bool &bad) {
+        if (parts == 0) {
+            left = 0;
+            return;
+        }
+        left -= tile.n + kAtItemCost - off;
         if (left <= 0) return;
+        at += tile.n + kAtItemCost;
+        off = 0;
         if (++h < p.H) return;
         h = 0;
         if (++rt >= nrt) {
@@ -254,9 +317,8 @@ struct AtPiece {
     int n, s_first;                    // steps, and the first one's number in its sequence
     int row, rows, len;                // first packed row and row count of the sequence, its length
     int rt, h;
-    int whole, slot;                   // covers its item; else where its sums go
-    int c0, c1;                        // parts that share the item
-    int pad;
+    int c0, c1;                        // CTAs that share the item
+    int pad[3];
 };
 constexpr int kAtPieces = 4;           // handed over ahead
 constexpr int kAtSmemPerSm = 228 * 1024;
@@ -280,6 +342,9 @@ struct AtShape {
     // the ring takes what a CTA's share of the 228 KB leaves (1 KB a CTA is the system's)
     static constexpr int kRoom = (int)((kAtSmemPerSm / kCtas - 1024 - kFixedBytes) / kStageBytes);
     static constexpr int kStages = kRoom < 16 ? kRoom : 16;
+    // lanes that share a row when parts are joined: a power of two, at least one row a thread
+    static constexpr int kJoinLanes = 32 * WARPS / kRows >= 16 ? 16 : 32 * WARPS / kRows >= 8 ? 8 : 32 * WARPS / kRows >= 4 ? 4 : 1;
+    static_assert(kRows <= 32 * WARPS, "a thread joins the maxima of one row");
     static constexpr bool kTagged = kStages % kGroups != 0;
     static constexpr size_t kSmem = kFixedBytes + kStages * kStageBytes;
     static_assert(kStages >= kGroups, "each warp needs a stage of its own");
@@ -332,23 +397,20 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
         walk.init(p, kRows, bad);
         int ps = 0;                    // piece slot
         uint32_t pparity = 1;
-        auto hand = [&](int n) {
+        auto hand = [&](int lo, int hi, int c0, int c1) {
             if (!mbar_wait_bounded(pfree_a + 8 * ps, pparity, p.wait_rounds)) return false;
             if (lane == 0) {
                 AtPiece &q = pieces[ps];
-                q.n = n;
-                if (n > 0) {
-                    const long long lo = walk.at - walk.off;             // the item's first step of the line
-                    q.s_first = walk.tile.s0 + walk.off;
+                q.n = hi - lo;
+                if (hi > lo) {
+                    q.s_first = walk.tile.s0 + lo;
                     q.row = walk.seq.row;
                     q.rows = walk.seq.n;
                     q.len = walk.seq.len;
                     q.rt = walk.rt;
                     q.h = walk.h;
-                    q.whole = n == walk.tile.n;
-                    q.slot = 2 * blockIdx.x + (walk.off > 0 ? 0 : 1);
-                    q.c0 = q.whole ? 0 : walk.part_of(lo);
-                    q.c1 = q.whole ? 0 : walk.part_of(lo + walk.tile.n - 1);
+                    q.c0 = c0;
+                    q.c1 = c1;
                 }
                 mbar_arrive(pfull_a + 8 * ps);
             }
@@ -368,8 +430,14 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
         uint32_t parity = 1;           // of the free barriers: the first round passes at once
         bool ok = true;
         while (walk.left > 0 && ok) {
-            const int n = walk.piece(), s_first = walk.tile.s0 + walk.off;
-            ok = hand(n) && !p.inject;
+            int lo, hi, c0, c1;
+            walk.piece(lo, hi, c0, c1);
+            if (hi <= lo) {
+                walk.next(p, kRows, bad);
+                continue;
+            }
+            const int n = hi - lo, s_first = walk.tile.s0 + lo;
+            ok = hand(lo, hi, c0, c1) && !p.inject;
             const int32_t *table = p.tok.table + (long long)walk.b * p.tok.max_pages;
             int pid[2], pid_next[2];   // page of each half of this lane's step, -1: no token there
             float sk[2], sv[2], sk_next[2], sv_next[2];
@@ -451,9 +519,9 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
                     sv[i] = sv_next[i];
                 }
             }
-            walk.next(p, kRows, n, bad);
+            walk.next(p, kRows, bad);
         }
-        if (ok) ok = hand(0);
+        if (ok) ok = hand(0, 0, 0, 0);
         if (bad) atomicOr(p.status, kKvStatusIndex);
         if (!ok) {                     // a consumer gave up: record it, let the copies in flight land
             if (lane == 0) atomicOr(p.status, kAtStatusWait);
@@ -671,8 +739,9 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
         asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
         // read again rather than held in registers through the steps
         const int e0 = pc.rt * kRows, erows = min(kRows, pc.rows * p.G - e0), eh = pc.h, erow = pc.row;
-        const bool whole = pc.whole;
-        const int slot = pc.slot;
+        const int c0 = pc.c0, c1 = pc.c1;
+        const bool whole = c0 == c1;
+        const int slot = 2 * blockIdx.x + ((int)blockIdx.x == c0);       // a CTA begins at most one shared item
         auto emit = [&](int r, int x, const float4 &v, float mm, float ll) {
             const int i = (e0 + r) / p.G, hq = eh * p.G + (e0 + r) - i * p.G;
             const float f = ll > 0.f ? 1.f / ll : 0.f;
@@ -714,7 +783,6 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
         }
         if (!whole) {
             // the last part of the item to finish joins them all
-            const int c0 = pc.c0, c1 = pc.c1;
             __threadfence();
             asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
             if (tid == 0) {
@@ -725,24 +793,47 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
             }
             asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
             if (flag[0]) {
+                // Up to a few dozen parts of 8 rows come from L2: many loads in flight, a dependent one nowhere.
+                // First the maxima, a few lanes a row; then every output's sum over the parts, in their order.
+                constexpr int kLanes = S::kJoinLanes, kBatch = 8;
+                auto slot_of = [&](int cc) { return (size_t)(2 * cc + (cc == c0)) * kRows; };
+                float *top = reinterpret_cast<float *>(mls);
+                {
+                    const int r = tid / kLanes;
+                    float mm = -INFINITY;
+                    if (r < erows) {
+#pragma unroll 4
+                        for (int cc = c0 + tid % kLanes; cc <= c1; cc += kLanes)
+                            mm = fmaxf(mm, __ldcg(p.part_ml + slot_of(cc) + r).x);
+                    }
+#pragma unroll
+                    for (int d = kLanes / 2; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+                    if (r < erows && tid % kLanes == 0) top[r] = mm;
+                }
+                asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
 #pragma unroll 1
                 for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
-                    const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
-                    float mm = -INFINITY;
-                    for (int cc = c0; cc <= c1; ++cc)
-                        mm = fmaxf(mm, __ldcg(p.part_ml + (size_t)(2 * cc + (cc == c0)) * kRows + r).x);
-                    const float ref = mm == -INFINITY ? 0.f : mm;
+                    const int r = i / (D / 4), x = i - r * (D / 4);
+                    const float mm = top[r], ref = mm == -INFINITY ? 0.f : mm;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                     float ll = 0.f;
-                    for (int cc = c0; cc <= c1; ++cc) {
-                        const size_t sl = 2 * cc + (cc == c0);
-                        const float2 ml = __ldcg(p.part_ml + sl * kRows + r);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.part) + (sl * kRows + r) * (D / 4) + x / 4);
-                        const float f = at_exp2(ml.x - ref);
-                        v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
-                        ll += ml.y * f;
+                    for (int cb = c0; cb <= c1; cb += kBatch) {
+                        float2 ml[kBatch];
+                        float4 y[kBatch];
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j) {
+                            const size_t at = slot_of(min(cb + j, c1)) + r;
+                            ml[j] = __ldcg(p.part_ml + at);
+                            y[j] = __ldcg(reinterpret_cast<const float4 *>(p.part) + at * (D / 4) + x);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j) {
+                            const float f = cb + j <= c1 ? at_exp2(ml[j].x - ref) : 0.f;
+                            v.x += y[j].x * f; v.y += y[j].y * f; v.z += y[j].z * f; v.w += y[j].w * f;
+                            ll += ml[j].y * f;
+                        }
                     }
-                    emit(r, x, v, mm, ll);
+                    emit(r, 4 * x, v, mm, ll);
                 }
             }
         }

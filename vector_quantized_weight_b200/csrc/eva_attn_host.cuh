@@ -482,7 +482,7 @@ eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t
     p.G = d.q_heads / d.kv_heads;
     p.window = d.window;
     p.out_f32 = d.out_dtype == EVA_F32;
-    p.min_steps = 8;
+    p.min_steps = 16;
     p.inject = h->inject_wait_rounds > 0;
     p.wait_rounds = p.inject ? h->inject_wait_rounds : kWaitRounds;
     h->inject_wait_rounds = 0;
