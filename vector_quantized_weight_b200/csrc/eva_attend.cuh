@@ -9,7 +9,7 @@
 // What bounds it: a decode step reads each cached byte once for a handful of
 // multiplications, so bytes; everything else has to fit beside the stream.
 //  - Codes become f16 exactly (int8: a byte under exponent 2^10, minus 1152;
-//    e4m3: sign and magnitude shifted into an f16's fields, times 2^8) and go
+//    e4m3: the conversion instruction) and go
 //    to the tensor cores as the A operand: 16 tokens x 16 dimensions of keys,
 //    16 dimensions x 16 tokens of values.  Rows are the MMA's N (8 at a time),
 //    so a decode step of one to eight queries a key head wastes nothing, and
@@ -23,14 +23,18 @@
 //    the sum of the softmax gets w_j / sv.  w_j is rounded to f16 (one
 //    2^-12 error a weight, averaged over the keys); all sums and statistics are
 //    fp32.
-//  - One warp streams: it looks pages up, and copies 32 tokens of keys and
-//    values a step into a ring of shared memory (TMA, 128-byte swizzle: both
-//    ldmatrix patterns are free of bank conflicts).  A page id outside the
-//    cache is never used as an address: its tokens count as masked and the
-//    status word is set.
+//  - One warp of a CTA walks the work, looks pages and scales up, 32 steps at a
+//    time, one a lane, and copies each step's codes (TMA, swizzled: both
+//    ldmatrix patterns are free of bank conflicts) into a ring in shared
+//    memory; the others take turns at the steps.  (Copies issued by the warp
+//    that needs them, into buffers of its own, measured 10 us slower on 268 MB
+//    at 64 sequences: the issue then sits between a step's products.)  A page
+//    id outside the cache is never used as an address: its tokens count as
+//    masked and the status word is set.
 //  - Work is cut on the device, because only the device knows the lengths
-//    (AtWalk).  An item (sequence, row tile, key head) that several CTAs share is joined by the last of them to finish, in the order
-//    of the parts, so results do not depend on timing.
+//    (AtWalk).  An item (sequence, row tile, key head) that several CTAs share
+//    is joined by the last of them to finish, in the order of the parts, so
+//    results do not depend on timing.
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -40,7 +44,6 @@
 
 namespace eva {
 
-constexpr int kAtStep = 32;            // tokens a step
 constexpr int kAtStatusWait = 1;       // status bit: a bounded wait gave up
 
 struct AttendParams {
@@ -52,7 +55,7 @@ struct AttendParams {
     float *lse;                        // [T][Hq] or null
     float *part;                       // [2 grid][rows][D] unnormalised outputs of shared items
     float2 *part_ml;                   // [2 grid][rows] maximum (base 2) and sum
-    int *counters;                     // [grid], zero between calls
+    int *counters;                     // [3][grid], zero between calls
     int *status;
     int Hq, H, G;                      // query heads, key heads, queries a key head
     int window, out_f32, min_steps, wait_rounds;
@@ -84,6 +87,34 @@ __device__ __forceinline__ void at_ldsm_t(uint32_t a, uint32_t (&r)[4]) {
                  : "r"(a)
                  : "memory");
 }
+// mbar_wait_bounded with its loop inside the statement: no reconvergence code around it.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, int rounds) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\t"
+        "mov.b32 n, %3;\n\t"
+        "LOOP:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.s32 n, n, 1;\n\t"
+        "setp.gt.s32 q, n, 0;\n\t"
+        "@q bra LOOP;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(rounds)
+        : "memory");
+    return ok != 0;
+}
+// A counter in shared memory that one warp advances and the others read.
+__device__ __forceinline__ void at_publish(uint32_t a, int v) {
+    asm volatile("st.release.cta.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ int at_published(uint32_t a) {
+    int v;
+    asm volatile("ld.acquire.cta.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t at_transpose(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -102,38 +133,40 @@ __device__ __forceinline__ float at_exp2(float x) {
 
 // Four codes -> two pairs of f16: neighbours (b0 b1, b2 b3: dimensions of a
 // key) or every other (b0 b2, b1 b3: a dimension of two tokens' values).
+// (Leaving int8 values 1152 too large and taking 1152 times the sum of the
+// weights off at the end would save two subtractions in five operations, but
+// the tensor cores' sums truncate, and over a long context that bias is no
+// longer small beside an average of values of both signs.)
 template <bool E4M3>
 struct AtCode;
 template <>
 struct AtCode<false> {
-    static constexpr float kUnit = 1.f;
-    static __device__ __forceinline__ uint32_t finish(uint32_t w) {
+    static __device__ __forceinline__ uint32_t exact(uint32_t w) {
         const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&w), __half2half2(__ushort_as_half(0x6480)));
         return *reinterpret_cast<const uint32_t *>(&h);
     }
-    template <uint32_t A, uint32_t B>
-    static __device__ __forceinline__ void two(uint32_t x, uint32_t &a, uint32_t &b) {
+    static __device__ __forceinline__ void key(uint32_t x, uint32_t &a, uint32_t &b) {
         x ^= 0x80808080u;
-        a = finish(__byte_perm(x, 0x64646464u, A));
-        b = finish(__byte_perm(x, 0x64646464u, B));
+        a = exact(__byte_perm(x, 0x64646464u, 0x4140));
+        b = exact(__byte_perm(x, 0x64646464u, 0x4342));
     }
-    static __device__ __forceinline__ void near(uint32_t x, uint32_t &a, uint32_t &b) { two<0x4140, 0x4342>(x, a, b); }
-    static __device__ __forceinline__ void apart(uint32_t x, uint32_t &a, uint32_t &b) { two<0x4240, 0x4341>(x, a, b); }
+    static __device__ __forceinline__ void value(uint32_t x, uint32_t &a, uint32_t &b) {
+        x ^= 0x80808080u;
+        a = exact(__byte_perm(x, 0x64646464u, 0x4240));
+        b = exact(__byte_perm(x, 0x64646464u, 0x4341));
+    }
 };
 template <>
 struct AtCode<true> {
-    static constexpr float kUnit = 256.f;
-    static __device__ __forceinline__ uint32_t finish(uint32_t w) {
-        return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+    static __device__ __forceinline__ void key(uint32_t x, uint32_t &a, uint32_t &b) {
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(a), "=r"(b)
+            : "r"(x));
     }
-    static __device__ __forceinline__ void near(uint32_t x, uint32_t &a, uint32_t &b) {
-        a = finish(__byte_perm(x, 0u, 0x1404));
-        b = finish(__byte_perm(x, 0u, 0x3424));
-    }
-    static __device__ __forceinline__ void apart(uint32_t x, uint32_t &a, uint32_t &b) {
-        a = finish(__byte_perm(x, 0u, 0x2404));
-        b = finish(__byte_perm(x, 0u, 0x3414));
-    }
+    static __device__ __forceinline__ void value(uint32_t x, uint32_t &a, uint32_t &b) { key(__byte_perm(x, 0u, 0x3120), a, b); }
 };
 
 // ------------------------------------------------------- the line of steps
@@ -143,13 +176,14 @@ struct AtCode<true> {
 struct AtTile {
     int s0, n;
 };
+template <int TS>
 __device__ __forceinline__ AtTile at_tile(const KvSeq &s, int rt, int rows, int G, int window) {
     const int r0 = rt * rows, r1 = min(r0 + rows, s.n * G) - 1;
     const int hi = s.len - s.n + r1 / G;
     const int lo = window > 0 ? max(0, s.len - s.n + r0 / G - window + 1) : 0;
     AtTile t;
-    t.s0 = hi < lo ? 0 : lo / kAtStep;
-    t.n = hi < lo ? 1 : hi / kAtStep - t.s0 + 1;
+    t.s0 = hi < lo ? 0 : lo / TS;
+    t.n = hi < lo ? 1 : hi / TS - t.s0 + 1;
     return t;
 }
 __device__ __forceinline__ int at_tiles(const KvSeq &s, int rows, int G) { return (s.n * G + rows - 1) / rows; }
@@ -164,6 +198,7 @@ __device__ __forceinline__ int at_tiles(const KvSeq &s, int rows, int G) { retur
 // besides its own (starting and finishing it costs a CTA about that), and
 // every CTA takes an equal stretch, whatever the items' borders.
 constexpr int kAtItemCost = 4;
+template <int TS>
 struct AtWalk {
     long long total, at;               // the line's length, the current item's place in it
     int left;                          // of this CTA's stretch from the current place on (few items: 1 or 0)
@@ -192,7 +227,7 @@ struct AtWalk {
         for (int b0 = 0; b0 < p.tok.B; b0 += 32) {
             const KvSeq s = seq_of(b0);
             const int n = at_tiles(s, rows, p.G);
-            for (int t = 0; t < n; ++t) steps += at_tile(s, t, rows, p.G, p.window).n;
+            for (int t = 0; t < n; ++t) steps += at_tile<TS>(s, t, rows, p.G, p.window).n;
             items += n;
         }
 #pragma unroll
@@ -226,7 +261,7 @@ struct AtWalk {
             const KvSeq s = seq_of(b0);
             long long w = 0;
             for (int t = 0, n = at_tiles(s, rows, p.G); t < n; ++t) {
-                const int m = at_tile(s, t, rows, p.G, p.window).n;
+                const int m = at_tile<TS>(s, t, rows, p.G, p.window).n;
                 w += few ? cuts(m, S) : m + kAtItemCost;
             }
             w *= p.H;
@@ -252,7 +287,7 @@ struct AtWalk {
         long long in = place - before;
         int w = 1;
         for (rt = 0;; ++rt) {
-            tile = at_tile(seq, rt, rows, p.G, p.window);
+            tile = at_tile<TS>(seq, rt, rows, p.G, p.window);
             w = few ? cuts(tile.n, S) : tile.n + kAtItemCost;
             if (in < (long long)w * p.H || rt + 1 >= nrt) break;
             in -= (long long)w * p.H;
@@ -296,7 +331,7 @@ struct AtWalk {
             while (seq.n == 0 && b + 1 < p.tok.B);
             nrt = at_tiles(seq, rows, p.G);
         }
-        tile = at_tile(seq, rt, rows, p.G, p.window);
+        tile = at_tile<TS>(seq, rt, rows, p.G, p.window);
     }
     // the part that holds step s of the line
     __device__ __forceinline__ int part_of(long long s) const { return (int)(((s + 1) * parts - 1) / total); }
@@ -304,106 +339,167 @@ struct AtWalk {
 
 // --------------------------------------------------------------- the kernel
 
-// What the streaming warp leaves beside a step's codes, for each half (16
-// tokens) of the step: the score's factor, log2 of the value scale, and one
-// over it; factor < 0 marks tokens that are not there.
+// What the walking warp leaves beside a step's codes, for each 16 tokens: the
+// score's factor (negative: no token there), log2 of the value scale, and one
+// over it.
 struct AtScales {
     float sk[2], lsv[2], rsv[2];
     int tag, pad;                      // the step's number in its CTA
 };
-
-// One piece of the line, as the streaming warp hands it to the others (n 0: no more).
+// A piece of work: the steps t0 .. t0 + n - 1 of the CTA (n 0: no more).
 struct AtPiece {
-    int n, s_first;                    // steps, and the first one's number in its sequence
+    int t0, n, s_first;                // and the first one's number in its sequence
     int row, rows, len;                // first packed row and row count of the sequence, its length
     int rt, h;
     int c0, c1;                        // CTAs that share the item
-    int pad[3];
+    int pad[2];
 };
 constexpr int kAtPieces = 4;           // handed over ahead
 constexpr int kAtSmemPerSm = 228 * 1024;
+constexpr int kAtSegment = 8;          // parts that are joined at a time
 
-template <int D, int NT, int WR, int WARPS>
+template <int D, int NT, int WARPS, int CTAS>
 struct AtShape {
-    static constexpr int kRows = 8 * NT * WR;              // rows of an item
-    static constexpr int kGroups = WARPS / WR;             // warps that take different steps
-    static constexpr int kStepBytes = 2 * kAtStep * D;
+    static constexpr int kRows = 8 * NT;                   // rows of an item
+    static constexpr int kStep = D > 128 ? 16 : 32;        // tokens a step: 8 KB of keys and values, 4 at D = 64
+    static constexpr int kStepBytes = 2 * kStep * D;
     static constexpr int kThreads = 32 * (WARPS + 1);
-    // Resident CTAs an SM, by registers: warps are dealt to four schedulers of 16384 registers each, so 16 warps
-    // get 128 each, 12 get 168, 8 get 255.
-    static constexpr int kCtas = NT * D <= 128 ? (WARPS < 6 ? 3 : 2) : NT * D <= 256 && WARPS < 6 ? 2 : 1;
     static constexpr int kQStride = D + 16;                // halves; 8 g + 2 c words: no conflicts
     static constexpr int kOStride = D + 4;                 // floats; 8 c + 2 g words: no conflicts
     static constexpr size_t kQBytes = (size_t)kRows * kQStride * 2;
-    static constexpr size_t kOBytes = (size_t)kGroups * kRows * kOStride * 4;
-    static constexpr size_t kMlBytes = (size_t)kGroups * kRows * 8;
+    static constexpr size_t kOBytes = (size_t)WARPS * kRows * kOStride * 4;
+    static constexpr size_t kMlBytes = (size_t)WARPS * kRows * 8;
+    static constexpr size_t kFixedBytes = 1024 + kQBytes + kOBytes + kMlBytes + kAtPieces * (sizeof(AtPiece) + 16) + 128;
     static constexpr size_t kStageBytes = kStepBytes + sizeof(AtScales) + 16;
-    static constexpr size_t kFixedBytes = 1024 + kQBytes + kOBytes + kMlBytes + kAtPieces * (sizeof(AtPiece) + 16) + 64;
     // the ring takes what a CTA's share of the 228 KB leaves (1 KB a CTA is the system's)
-    static constexpr int kRoom = (int)((kAtSmemPerSm / kCtas - 1024 - kFixedBytes) / kStageBytes);
+    static constexpr int kRoom = (int)((kAtSmemPerSm / CTAS - 1024 - kFixedBytes) / kStageBytes);
     static constexpr int kStages = kRoom < 16 ? kRoom : 16;
-    // lanes that share a row when parts are joined: a power of two, at least one row a thread
-    static constexpr int kJoinLanes = 32 * WARPS / kRows >= 16 ? 16 : 32 * WARPS / kRows >= 8 ? 8 : 32 * WARPS / kRows >= 4 ? 4 : 1;
-    static_assert(kRows <= 32 * WARPS, "a thread joins the maxima of one row");
-    static constexpr bool kTagged = kStages % kGroups != 0;
+    static constexpr bool kTagged = kStages % WARPS != 0;
     static constexpr size_t kSmem = kFixedBytes + kStages * kStageBytes;
-    static_assert(kStages >= kGroups, "each warp needs a stage of its own");
+    static_assert(kStages >= WARPS, "each warp needs a stage of its own");
+    // lanes that share a row when parts are joined: a power of two, at least one row a thread
+    static constexpr int kJoinLanes = 32 * WARPS / kRows >= 16 ? 16 : 32 * WARPS / kRows >= 8 ? 8 : 4;
+    static_assert(kRows * kJoinLanes <= 32 * WARPS, "a few lanes join the maxima of a row");
 };
 
-template <int D, int NT, int WR, int WARPS, bool E4M3>
-__global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::kCtas)
+// Resident CTAs an SM: warps are dealt to four schedulers of 16384 registers
+// each, so 16 warps get 128 registers each, 12 get 168, 8 get 255.
+template <int D, int NT, int WARPS, int CTAS, bool E4M3>
+__global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
     eva_attend_kernel(const __grid_constant__ AttendMaps maps, AttendParams p) {
-    using S = AtShape<D, NT, WR, WARPS>;
-    constexpr int kRows = S::kRows, kGroups = S::kGroups, kChunks = D / 16, stages = S::kStages;
-    constexpr int kBarConsumers = 1;
-    // shared memory: ring | scales | full and free barriers | pieces and theirs | queries | outputs | statistics
+    using S = AtShape<D, NT, WARPS, CTAS>;
+    constexpr int kRows = S::kRows, kChunks = D / 16, kStep = S::kStep, MT = kStep / 16, kStages = S::kStages;
+    // shared memory: ring | scales | pieces | queries | outputs | statistics | barriers (stages full and free, pieces
+    // full and free, the warps') | flags
     const uint32_t base0 = (uint32_t)__cvta_generic_to_shared(eva_smem);
-    const uint32_t skip = ((base0 + 1023) & ~1023u) - base0;
-    uint8_t *ring = eva_smem + skip;
-    const uint32_t ring_a = base0 + skip;
-    AtScales *scales = reinterpret_cast<AtScales *>(ring + (size_t)stages * S::kStepBytes);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(scales + stages);
-    const uint32_t full_a = (uint32_t)__cvta_generic_to_shared(bars), free_a = full_a + 8 * stages;
-    uint64_t *pbars = bars + 2 * stages;
-    const uint32_t pfull_a = free_a + 8 * stages, pfree_a = pfull_a + 8 * kAtPieces;
-    AtPiece *pieces = reinterpret_cast<AtPiece *>(pbars + 2 * kAtPieces);
+    const uint32_t skip = ((base0 + 1023) & ~1023u) - base0, ring_a = base0 + skip;
+    AtScales *scales = reinterpret_cast<AtScales *>(eva_smem + skip + kStages * S::kStepBytes);
+    AtPiece *pieces = reinterpret_cast<AtPiece *>(scales + kStages);
     __half *qs = reinterpret_cast<__half *>(pieces + kAtPieces);
     float *os = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(qs) + S::kQBytes);
     float2 *mls = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(os) + S::kOBytes);
-    // [0] this CTA joins the item, [1] a warp of this CTA gave up a wait
-    volatile int *flag = reinterpret_cast<volatile int *>(reinterpret_cast<uint8_t *>(mls) + S::kMlBytes);
+    const uint32_t full_a = (uint32_t)__cvta_generic_to_shared(reinterpret_cast<uint8_t *>(mls) + S::kMlBytes);
+    const uint32_t free_a = full_a + 8 * kStages, pfull_a = free_a + 8 * kStages, pfree_a = pfull_a + 8 * kAtPieces;
+    const uint32_t meet_a = pfree_a + 8 * kAtPieces;
+    volatile int *flag = reinterpret_cast<volatile int *>(eva_smem + (meet_a + 8 - base0));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < stages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             scales[i].tag = -1;
-            mbar_init(full_a + 8 * i, 1);
-            mbar_init(free_a + 8 * i, WR);
+            mbar_init(full_a + 8 * i, 2);      // the copies' bytes, and the scales
+            mbar_init(free_a + 8 * i, 1);
         }
         for (int i = 0; i < kAtPieces; ++i) {
             mbar_init(pfull_a + 8 * i, 1);
             mbar_init(pfree_a + 8 * i, WARPS);
         }
-        flag[1] = 0;
+        mbar_init(meet_a, WARPS);
     }
     __syncthreads();
     pdl_wait();
     pdl_launch();
 
     if (warp == WARPS) {
-        // ------------------------------------------------ the streaming warp
-        bool bad = false;
-        AtWalk walk;
+        // -------------------------------------------------- the walking warp
+        bool bad = false, ok = true;
+        AtWalk<kStep> walk;
         walk.init(p, kRows, bad);
-        int ps = 0;                    // piece slot
+        const int page = p.tok.page;
+        const bool split = page < kStep;                   // a step's halves lie on two pages
+        const int box = split ? 16 : kStep;
+        int t = 0, st = 0, ahead = 0;  // steps so far, the next one's stage, steps copied before their scales were known
+        uint32_t parity = 1;           // of the free barriers: the first round passes at once
+        int ps = 0;                    // the next piece's place
         uint32_t pparity = 1;
-        auto hand = [&](int lo, int hi, int c0, int c1) {
-            if (!mbar_wait_bounded(pfree_a + 8 * ps, pparity, p.wait_rounds)) return false;
-            if (lane == 0) {
-                AtPiece &q = pieces[ps];
-                q.n = hi - lo;
-                if (hi > lo) {
-                    q.s_first = walk.tile.s0 + lo;
+        while (ok && walk.left > 0) {
+            int lo, hi, c0, c1;
+            walk.piece(lo, hi, c0, c1);
+            const int s_first = walk.tile.s0 + lo, n = hi - lo;
+            if (n > 0) {
+                const int32_t *table = p.tok.table + (long long)walk.b * p.tok.max_pages;
+                int pid[2] = {-1, -1}, pid_next[2];        // pages of this lane's step, -1: no token there
+                auto look = [&](int s, int (&id)[2]) {
+                    id[0] = id[1] = -1;
+                    if (s >= n) return;
+                    const int tok0 = (s_first + s) * kStep;
+                    if (tok0 < walk.seq.len) id[0] = table[tok0 / page];
+                    if (MT > 1 && tok0 + 16 < walk.seq.len) id[1] = split ? table[tok0 / page + 1] : id[0];
+                };
+                auto check = [&](int s, int (&id)[2]) {    // a page outside the cache: no token there, and say so
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        if (id[i] >= 0 && id[i] < p.tok.num_pages) continue;
+                        if (s < n && (s_first + s) * kStep + 16 * i < walk.seq.len) bad = true;
+                        id[i] = -1;
+                    }
+                };
+                auto scale = [&](const int (&id)[2], float (&k)[2], float (&v)[2]) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        const bool there = id[i] >= 0;
+                        k[i] = there ? p.k_scale[(long long)id[i] * p.H + walk.h] : -1.f;
+                        v[i] = there ? p.v_scale[(long long)id[i] * p.H + walk.h] : 1.f;
+                    }
+                };
+                auto copy = [&](int s, int stage) {        // this lane's step s into a stage
+                    const bool two = MT > 1 && split && pid[1] >= 0;
+                    const uint32_t bytes = (uint32_t)(((pid[0] >= 0) + two) * 2 * box * D);
+                    const uint32_t bar = full_a + 8 * stage, dst = ring_a + stage * S::kStepBytes;
+                    if (bytes)
+                        mbar_arrive_expect_tx(bar, bytes);
+                    else
+                        mbar_arrive(bar);
+                    const int y0 = (pid[0] * p.H + walk.h) * page + ((s_first + s) * kStep & (page - 1));
+                    const int y1 = (pid[1] * p.H + walk.h) * page;
+#pragma unroll
+                    for (int x = 0; x < D; x += 128) {     // a column half of 128 bytes is [kStep][128]
+                        const uint32_t o = dst + (uint32_t)(x * kStep), o2 = o + (uint32_t)(16 * (D < 128 ? D : 128));
+                        if (pid[0] >= 0) {
+                            at_tma_2d(o, &maps.k, x, y0, bar);
+                            at_tma_2d(o + kStep * D, &maps.v, x, y0, bar);
+                        }
+                        if (two) {
+                            at_tma_2d(o2, &maps.k, x, y1, bar);
+                            at_tma_2d(o2 + kStep * D, &maps.v, x, y1, bar);
+                        }
+                    }
+                };
+                look(lane, pid);
+                check(lane, pid);
+                if (t == 0 && !p.inject) {
+                    ahead = min(min(n, 32), kStages);
+                    if (lane < ahead) copy(lane, lane);
+                }
+                float sk[2], sv[2], sk_next[2] = {}, sv_next[2] = {};
+                scale(pid, sk, sv);
+                ok = at_wait(pfree_a + 8 * ps, pparity, p.wait_rounds);
+                if (!ok) break;
+                if (lane == 0) {
+                    AtPiece &q = pieces[ps];
+                    q.t0 = t;
+                    q.n = n;
+                    q.s_first = s_first;
                     q.row = walk.seq.row;
                     q.rows = walk.seq.n;
                     q.len = walk.seq.len;
@@ -411,259 +507,208 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
                     q.h = walk.h;
                     q.c0 = c0;
                     q.c1 = c1;
+                    mbar_arrive(pfull_a + 8 * ps);
                 }
-                mbar_arrive(pfull_a + 8 * ps);
-            }
-            __syncwarp();
-            if (++ps == kAtPieces) {
-                ps = 0;
-                pparity ^= 1;
-            }
-            return true;
-        };
-        // Each lane looks up the pages and scales of one step of the next 32 and issues that step's copies itself, so
-        // a step costs the warp one wait and a few instructions; the following 32 steps' lookups are in flight
-        // meanwhile.
-        const int page = p.tok.page, boxes = page < kAtStep ? 2 : 1;     // boxes of a step
-        const int box_rows = kAtStep / boxes;
-        int st = 0, t = 0;
-        uint32_t parity = 1;           // of the free barriers: the first round passes at once
-        bool ok = true;
-        while (walk.left > 0 && ok) {
-            int lo, hi, c0, c1;
-            walk.piece(lo, hi, c0, c1);
-            if (hi <= lo) {
-                walk.next(p, kRows, bad);
-                continue;
-            }
-            const int n = hi - lo, s_first = walk.tile.s0 + lo;
-            ok = hand(lo, hi, c0, c1) && !p.inject;
-            const int32_t *table = p.tok.table + (long long)walk.b * p.tok.max_pages;
-            int pid[2], pid_next[2];   // page of each half of this lane's step, -1: no token there
-            float sk[2], sv[2], sk_next[2], sv_next[2];
-            auto look = [&](int s, int (&id)[2]) {
-                id[0] = id[1] = -1;
-                if (s >= n) return;
-                const int tok0 = (s_first + s) * kAtStep;
-                if (tok0 < walk.seq.len) id[0] = table[tok0 / page];
-                if (tok0 + 16 < walk.seq.len) id[1] = boxes == 1 ? id[0] : table[tok0 / page + 1];
-            };
-            auto scale = [&](int s, int (&id)[2], float (&k)[2], float (&v)[2]) {
+                if (++ps == kAtPieces) {
+                    ps = 0;
+                    pparity ^= 1;
+                }
+                ok = !p.inject;
+                for (int s0 = 0; s0 < n && ok; s0 += 32) {
+                    look(s0 + 32 + lane, pid_next);        // in flight while these steps go out
+                    AtScales sc = {};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (id[i] < 0 || id[i] >= p.tok.num_pages) {
-                        if (s < n && (s_first + s) * kAtStep + 16 * i < walk.seq.len) bad = true;
-                        id[i] = -1;
+                    for (int i = 0; i < MT; ++i) {
+                        const float v = fmaxf(sv[i], 1e-30f);
+                        sc.sk[i] = sk[i];
+                        sc.lsv[i] = log2f(v);
+                        sc.rsv[i] = 1.f / v;
                     }
-                    const bool there = id[i] >= 0;
-                    k[i] = there ? p.k_scale[(long long)id[i] * p.H + walk.h] : -1.f;
-                    v[i] = there ? p.v_scale[(long long)id[i] * p.H + walk.h] : 1.f;
-                }
-            };
-            look(lane, pid);
-            scale(lane, pid, sk, sv);
-            for (int s0 = 0; s0 < n && ok; s0 += 32) {
-                look(s0 + 32 + lane, pid_next);
-                AtScales sc = {};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float e = fmaxf(sv[i] * AtCode<E4M3>::kUnit, 1e-30f);
-                    sc.sk[i] = pid[i] < 0 ? -1.f : sk[i] * AtCode<E4M3>::kUnit;
-                    sc.lsv[i] = log2f(e);
-                    sc.rsv[i] = 1.f / e;
-                }
-                const int slot = (s_first + s0 + lane) * kAtStep & (page - 1);
-                const int y0 = (pid[0] * p.H + walk.h) * page + (boxes == 2 ? 0 : slot), y1 = (pid[1] * p.H + walk.h) * page;
-                const bool two = boxes == 2 && pid[1] >= 0;
-                const uint32_t bytes = (uint32_t)(((pid[0] >= 0) + two) * 2 * box_rows * D);
-                const int steps = min(32, n - s0);
-                for (int i = 0; i < steps; ++i) {
-                    if (!mbar_wait_bounded(free_a + 8 * st, parity, p.wait_rounds)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == i) {
-                        const uint32_t bar = full_a + 8 * st, dst = ring_a + st * S::kStepBytes;
-                        sc.tag = t;
-                        scales[st] = sc;
-                        if (bytes)
-                            mbar_arrive_expect_tx(bar, bytes);
-                        else
-                            mbar_arrive(bar);
-#pragma unroll
-                        for (int x = 0; x < D; x += 128) {     // a column half of 128 bytes is [32][128]
-                            const uint32_t o = dst + (uint32_t)(x * kAtStep);
-                            if (pid[0] >= 0) {
-                                at_tma_2d(o, &maps.k, x, y0, bar);
-                                at_tma_2d(o + kAtStep * D, &maps.v, x, y0, bar);
-                            }
-                            if (two) {
-                                const uint32_t o2 = o + (uint32_t)(16 * (D < 128 ? D : 128));
-                                at_tma_2d(o2, &maps.k, x, y1, bar);
-                                at_tma_2d(o2 + kAtStep * D, &maps.v, x, y1, bar);
-                            }
+                    const int count = min(32, n - s0);
+                    for (int i = 0; i < count; ++i) {
+                        ok = at_wait(free_a + 8 * st, parity, p.wait_rounds);
+                        if (!ok) break;
+                        if (lane == i) {
+                            sc.tag = t;
+                            scales[st] = sc;
+                            mbar_arrive(full_a + 8 * st);
+                            if (t >= ahead) copy(s0 + i, st);
+                        }
+                        __syncwarp();
+                        if (++st == kStages) {
+                            st = 0;
+                            parity ^= 1;
+                        }
+                        ++t;
+                        if (i == 8) {
+                            check(s0 + 32 + lane, pid_next);
+                            scale(pid_next, sk_next, sv_next);
                         }
                     }
-                    __syncwarp();
-                    if (++st == stages) {
-                        st = 0;
-                        parity ^= 1;
-                    }
-                    ++t;
-                    if (i == 8) scale(s0 + 32 + lane, pid_next, sk_next, sv_next);
-                }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    pid[i] = pid_next[i];
-                    sk[i] = sk_next[i];
-                    sv[i] = sv_next[i];
+                    for (int i = 0; i < 2; ++i) {
+                        pid[i] = pid_next[i];
+                        sk[i] = sk_next[i];
+                        sv[i] = sv_next[i];
+                    }
                 }
             }
             walk.next(p, kRows, bad);
         }
-        if (ok) ok = hand(0, 0, 0, 0);
+        if (ok) ok = at_wait(pfree_a + 8 * ps, pparity, p.wait_rounds);
+        if (ok && lane == 0) {
+            pieces[ps].n = 0;
+            mbar_arrive(pfull_a + 8 * ps);
+        }
         if (bad) atomicOr(p.status, kKvStatusIndex);
-        if (!ok) {                     // a consumer gave up: record it, let the copies in flight land
+        if (!ok) {                     // another warp gave up: say so, let the copies in flight land
             if (lane == 0) atomicOr(p.status, kAtStatusWait);
-            for (int i = max(0, t - stages); i < t; ++i)
-                mbar_wait_bounded(full_a + 8 * (i % stages), (i / stages) & 1, p.wait_rounds);
+            for (; t < ahead; ++t)
+                if (lane == 0) mbar_arrive(full_a + 8 * t);
+            for (int i = max(0, t - kStages); i < t; ++i)
+                mbar_wait_bounded(full_a + 8 * (i % kStages), (i / kStages) & 1, p.wait_rounds);
         }
         return;
     }
 
-    // ------------------------------------------------------------ consumers
-    const int wr = warp % WR, grp = warp / WR;
+    // ---------------------------------------------------- the working warps
     const int g = lane >> 2, c = lane & 3, tid = threadIdx.x;      // tid < 32 * WARPS
-    constexpr float kLog2e = 1.4426950408889634f;
+    constexpr float kLog2e = 1.4426950408889634f, kLag = 8.f;
     const float zscale = p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e;
     const float zcap = p.cap * kLog2e;
-    int t0 = 0;                        // steps of earlier pieces: step t of this CTA is group t % kGroups's
-    int own = grp;                     // stage of this warp's next step, and its parity (stages >= kGroups)
-    uint32_t own_parity = 0;
-    int ps = 0;
-    uint32_t pparity = 0;
+
+    // All warps of the CTA have come here (and their shared-memory writes are seen); a bounded wait like the others,
+    // so that a warp that gave up leaves nobody waiting.
+    uint32_t meet_parity = 0;
+    auto meet = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(meet_a);
+        const bool r = at_wait(meet_a, meet_parity, p.wait_rounds);
+        meet_parity ^= 1;
+        return r;
+    };
+
+    auto addr = [&](uint32_t tile, int tok, int ch) {
+        if constexpr (D >= 128)
+            return tile + (uint32_t)((ch >> 3) * (kStep * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+        else
+            return tile + (uint32_t)(tok * 64 + ((ch ^ ((tok >> 1) & 3)) << 4));
+    };
+
+    float o[NT][kChunks][4], m[NT][2], l[NT][2];
+    int last[NT][2], pmin = 0, pmax = 0;       // the last key each row of this lane sees, and of the item's rows
+    int ps = 0, ct = warp;             // the piece's place; this warp's next step of the CTA
+    int own = warp;                    // and its stage, and that stage's parity
+    uint32_t pparity = 0, own_parity = 0;
+    bool ok = true;
     for (;;) {
-        const bool got = mbar_wait_bounded(pfull_a + 8 * ps, pparity, p.wait_rounds);
-        if (!got && lane == 0) flag[1] = 1;
-        const AtPiece &pc = pieces[ps];
-        const int n = got ? pc.n : 0, s_first = pc.s_first;
-        const KvSeq seq = {pc.row, pc.rows, pc.len};
-        const int r0 = pc.rt * kRows, nrows = min(kRows, seq.n * p.G - r0), h = pc.h;
-        // queries
-        auto qrow = [&](int r) {       // r: row of the item
-            const int i = (r0 + r) / p.G, hq = h * p.G + (r0 + r) - i * p.G;
-            return p.q + (seq.row + i) * p.ldq + (long long)hq * D;
-        };
-        if (n > 0) {
+        ok = at_wait(pfull_a + 8 * ps, pparity, p.wait_rounds);
+        if (!ok) break;
+        const AtPiece &bt = pieces[ps];
+        const int t_end = bt.t0 + bt.n, step0 = bt.s_first - bt.t0;
+        if (bt.n == 0) break;
+        {
+            const int r0 = bt.rt * kRows, nrows = min(kRows, bt.rows * p.G - r0), h = bt.h;
 #pragma unroll 1
             for (int i = tid; i < kRows * (D / 8); i += 32 * WARPS) {
                 const int r = i / (D / 8), x = i - r * (D / 8);
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < nrows) v = reinterpret_cast<const uint4 *>(qrow(r))[x];
+                if (r < nrows) {
+                    const int ti = (r0 + r) / p.G, hq = h * p.G + (r0 + r) - ti * p.G;
+                    v = reinterpret_cast<const uint4 *>(p.q + (bt.row + ti) * p.ldq + (long long)hq * D)[x];
+                }
                 *reinterpret_cast<uint4 *>(qs + r * S::kQStride + x * 8) = v;
             }
+            const int pos0 = bt.len - bt.rows;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    last[nt][e] = pos0 + (r0 + min(nrows - 1, nt * 8 + 2 * c + e)) / p.G;
+                    m[nt][e] = -INFINITY;
+                    l[nt][e] = 0.f;
+                }
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[nt][ch][e] = 0.f;
+            }
+            pmin = pos0 + r0 / p.G;
+            pmax = pos0 + (r0 + nrows - 1) / p.G;
+            ok = meet();
+            if (!ok) break;
         }
-        // all warps leave together: at the last piece, or when one has given up a wait
-        asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
-        if (n == 0 || flag[1]) break;
-        // positions: the last key each of this lane's rows sees
-        int last[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                last[nt][e] = seq.len - seq.n + (r0 + min(nrows - 1, (wr * NT + nt) * 8 + 2 * c + e)) / p.G;
-        const int pmin = seq.len - seq.n + r0 / p.G;                       // of the item's first row
-        const int pmax = seq.len - seq.n + (r0 + nrows - 1) / p.G;
-
-        float o[NT][kChunks][4], m[NT][2], l[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][ch][e] = 0.f;
-            m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.f;
-        }
-
-        for (int i = ((grp - t0) % kGroups + kGroups) % kGroups; i < n; i += kGroups) {
+        for (; ct < t_end; ct += WARPS) {
             const int st = own;
-            bool there = true;
             if constexpr (S::kTagged) {
                 // Where a stage passes from warp to warp, a warp may be two rounds behind, and a barrier's parity
                 // would tell it that its step is there.  Once the stage carries this step's number, every earlier
                 // round is over and the parity is unambiguous.
                 int tries = 0;
-                while (*reinterpret_cast<volatile int *>(&scales[st].tag) != t0 + i && ++tries < p.wait_rounds) __nanosleep(20);
-                there = tries < p.wait_rounds;
+                while (*reinterpret_cast<volatile int *>(&scales[st].tag) != ct && ++tries < p.wait_rounds) __nanosleep(20);
+                ok = tries < p.wait_rounds;
+                if (!ok) break;
             }
-            if (!there || !mbar_wait_bounded(full_a + 8 * st, own_parity, p.wait_rounds)) {
-                if (lane == 0) flag[1] = 1;
-                break;
-            }
-            own += kGroups;
-            if (own >= stages) {
-                own -= stages;
+            ok = at_wait(full_a + 8 * st, own_parity, p.wait_rounds);
+            if (!ok) break;
+            own += WARPS;
+            if (own >= kStages) {
+                own -= kStages;
                 own_parity ^= 1;
             }
-            const uint32_t kt = ring_a + st * S::kStepBytes, vt = kt + kAtStep * D;
+            const uint32_t kt = ring_a + st * S::kStepBytes, vt = kt + kStep * D;
             const AtScales sc = scales[st];
-            // S^T = K Q^T: 32 tokens x 8 NT rows
-            float z[NT][2][4];
+            // S^T = K Q^T: kStep tokens x 8 NT rows
+            float z[NT][MT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[nt][mt][e] = 0.f;
-            auto addr = [&](uint32_t tile, int tok, int ch) {
-                if constexpr (D >= 128)
-                    return tile + (uint32_t)((ch >> 3) * (kAtStep * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
-                else
-                    return tile + (uint32_t)(tok * 64 + ((ch ^ ((tok >> 1) & 3)) << 4));
-            };
 #pragma unroll
             for (int ch = 0; ch < kChunks; ch += 2) {
-                uint32_t a[2][2][4];   // [half of the tokens][chunk][fragment]
+                uint32_t a[MT][2][4];  // [16 tokens][chunk][fragment]
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
+                for (int mt = 0; mt < MT; ++mt) {
                     uint32_t r[4];
                     at_ldsm(addr(kt, mt * 16 + (lane & 15), ch + (lane >> 4)), r);
-                    AtCode<E4M3>::near(r[0], a[mt][0][0], a[mt][0][2]);
-                    AtCode<E4M3>::near(r[1], a[mt][0][1], a[mt][0][3]);
-                    AtCode<E4M3>::near(r[2], a[mt][1][0], a[mt][1][2]);
-                    AtCode<E4M3>::near(r[3], a[mt][1][1], a[mt][1][3]);
+                    AtCode<E4M3>::key(r[0], a[mt][0][0], a[mt][0][2]);
+                    AtCode<E4M3>::key(r[1], a[mt][0][1], a[mt][0][3]);
+                    AtCode<E4M3>::key(r[2], a[mt][1][0], a[mt][1][2]);
+                    AtCode<E4M3>::key(r[3], a[mt][1][1], a[mt][1][3]);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(
-                            qs + ((wr * NT + nt) * 8 + g) * S::kQStride + (ch + x) * 16 + 4 * c);
-                        at_mma(z[nt][0], a[0][x], v.x, v.y);
-                        at_mma(z[nt][1], a[1][x], v.x, v.y);
+                        const uint2 v = *reinterpret_cast<const uint2 *>(qs + (nt * 8 + g) * S::kQStride + (ch + x) * 16 + 4 * c);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) at_mma(z[nt][mt], a[mt][x], v.x, v.y);
                     }
                 }
             }
             // scores, in base 2 and with the value scale's logarithm added
-            const int tok0 = (s_first + i) * kAtStep;
-            const bool edge = tok0 + kAtStep - 1 > pmin || (p.window > 0 && tok0 <= pmax - p.window) ||
-                              sc.sk[0] < 0.f || sc.sk[1] < 0.f;
-            uint32_t pb[NT][2][2];
+            const int tok0 = (step0 + ct) * kStep;
+            const bool edge = tok0 + kStep - 1 > pmin || (p.window > 0 && tok0 <= pmax - p.window) || sc.sk[0] < 0.f ||
+                              (MT > 1 && sc.sk[MT - 1] < 0.f);
+            uint32_t pb[NT][MT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = z[nt][mt][e] * (sc.sk[mt] * zscale);
-                        if (p.cap > 0.f) x = zcap * (1.f - 2.f / (1.f + __expf(2.f * x)));
-                        z[nt][mt][e] = x + sc.lsv[mt];
+                        if (p.cap > 0.f) {
+                            const float x = z[nt][mt][e] * (sc.sk[mt] * zscale);
+                            z[nt][mt][e] = zcap - __fdividef(2.f * zcap, 1.f + __expf(2.f * x)) + sc.lsv[mt];
+                        } else {
+                            z[nt][mt][e] = z[nt][mt][e] * (sc.sk[mt] * zscale) + sc.lsv[mt];
+                        }
                     }
                 if (edge) {
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
+                    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int j = tok0 + mt * 16 + g + (e >> 1) * 8, pos = last[nt][e & 1];
@@ -673,14 +718,15 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(fmaxf(z[nt][0][e], z[nt][0][e + 2]), fmaxf(z[nt][1][e], z[nt][1][e + 2]));
+                    float mx = fmaxf(z[nt][0][e], z[nt][0][e + 2]);
+                    if (MT > 1) mx = fmaxf(mx, fmaxf(z[nt][MT - 1][e], z[nt][MT - 1][e + 2]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    const float mn = fmaxf(m[nt][e], mx);
-                    const float ref = mn == -INFINITY ? 0.f : mn;
-                    if (__any_sync(0xffffffffu, mn > m[nt][e])) {
-                        const float f = at_exp2(m[nt][e] - ref);       // 0 for the first keys
-                        l[nt][e] *= f;
+                    // The reference moves only when a score passes it by 2^8 (weights stay below 256): rescaling
+                    // the sums is as much work as a step's softmax.
+                    if (__any_sync(0xffffffffu, mx > m[nt][e] + kLag)) {
+                        const float mn = fmaxf(m[nt][e], mx), f = mn == -INFINITY ? 1.f : at_exp2(m[nt][e] - mn);
+                        l[nt][e] *= f;             // 0 for the first keys
 #pragma unroll
                         for (int ch = 0; ch < kChunks; ++ch) {
                             o[nt][ch][e] *= f;
@@ -688,8 +734,9 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
                         }
                         m[nt][e] = mn;
                     }
+                    const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
+                    for (int mt = 0; mt < MT; ++mt) {
                         const float w0 = at_exp2(z[nt][mt][e] - ref), w1 = at_exp2(z[nt][mt][e + 2] - ref);
                         z[nt][mt][e] = w0;
                         z[nt][mt][e + 2] = w1;
@@ -697,155 +744,201 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), AtShape<D, NT, WR, WARPS>::k
                     }
                 }
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const __half2 w = __floats2half2_rn(z[nt][mt][2 * e], z[nt][mt][2 * e + 1]);
                         pb[nt][mt][e] = at_transpose(*reinterpret_cast<const uint32_t *>(&w));
                     }
             }
-            // O^T += V^T P^T
+            if (E4M3 && edge) {
+                // what lies where no token is may be a NaN, and 0 * NaN is one: zeros instead
+                const int tok = lane % kStep;
+                if (tok0 + tok >= bt.len || (MT > 1 && tok >= 16 ? sc.sk[MT - 1] : sc.sk[0]) < 0.f)
+                    for (int x = 0; x < D; x += 16)
+                        *reinterpret_cast<uint4 *>(eva_smem + (vt - base0) + (D >= 128 ? (x >> 7) * (kStep * 128) + tok * 128 + (x & 127)
+                                                                                       : tok * 64 + x)) = make_uint4(0, 0, 0, 0);
+                __syncwarp();
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");       // before the stage's next copy
+            }
+            // O^T += V^T P^T; at 16 tokens a step one load brings two chunks of dimensions
+            if constexpr (MT > 1) {
 #pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) {
-                uint32_t r[4], a[2][4];
-                at_ldsm_t(addr(vt, lane, ch), r);
-                AtCode<E4M3>::apart(r[0], a[0][0], a[0][1]);
-                AtCode<E4M3>::apart(r[1], a[0][2], a[0][3]);
-                AtCode<E4M3>::apart(r[2], a[1][0], a[1][1]);
-                AtCode<E4M3>::apart(r[3], a[1][2], a[1][3]);
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    uint32_t r[4], a[2][4];
+                    at_ldsm_t(addr(vt, lane, ch), r);
+                    AtCode<E4M3>::value(r[0], a[0][0], a[0][1]);
+                    AtCode<E4M3>::value(r[1], a[0][2], a[0][3]);
+                    AtCode<E4M3>::value(r[2], a[1][0], a[1][1]);
+                    AtCode<E4M3>::value(r[3], a[1][2], a[1][3]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    at_mma(o[nt][ch], a[0], pb[nt][0][0], pb[nt][0][1]);
-                    at_mma(o[nt][ch], a[1], pb[nt][1][0], pb[nt][1][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        at_mma(o[nt][ch], a[0], pb[nt][0][0], pb[nt][0][1]);
+                        at_mma(o[nt][ch], a[1], pb[nt][MT - 1][0], pb[nt][MT - 1][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ch += 2) {
+                    uint32_t r[4], a[2][4];
+                    at_ldsm_t(addr(vt, lane & 15, ch + (lane >> 4)), r);
+                    AtCode<E4M3>::value(r[0], a[0][0], a[0][1]);
+                    AtCode<E4M3>::value(r[1], a[0][2], a[0][3]);
+                    AtCode<E4M3>::value(r[2], a[1][0], a[1][1]);
+                    AtCode<E4M3>::value(r[3], a[1][2], a[1][3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        at_mma(o[nt][ch], a[0], pb[nt][0][0], pb[nt][0][1]);
+                        at_mma(o[nt][ch + 1], a[1], pb[nt][0][0], pb[nt][0][1]);
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(free_a + 8 * st);
         }
-        // this piece's sums: the warps of different steps meet in shared memory
+        if (!ok) break;
+        {
+            // the piece's sums: the warps of different steps meet in shared memory
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
-                const int r = (wr * NT + nt) * 8 + 2 * c + e;
-                if (g == 0) mls[grp * kRows + r] = make_float2(m[nt][e], l[nt][e]);
-                float *dst = os + (size_t)(grp * kRows + r) * S::kOStride + 2 * g;
+                    for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+                    const int r = nt * 8 + 2 * c + e;
+                    if (g == 0) mls[warp * kRows + r] = make_float2(m[nt][e], l[nt][e]);
+                    float *dst = os + (size_t)(warp * kRows + r) * S::kOStride + 2 * g;
 #pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch)
-                    *reinterpret_cast<float2 *>(dst + ch * 16) = make_float2(o[nt][ch][e], o[nt][ch][e + 2]);
-            }
-        asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
-        // read again rather than held in registers through the steps
-        const int e0 = pc.rt * kRows, erows = min(kRows, pc.rows * p.G - e0), eh = pc.h, erow = pc.row;
-        const int c0 = pc.c0, c1 = pc.c1;
-        const bool whole = c0 == c1;
-        const int slot = 2 * blockIdx.x + ((int)blockIdx.x == c0);       // a CTA begins at most one shared item
-        auto emit = [&](int r, int x, const float4 &v, float mm, float ll) {
-            const int i = (e0 + r) / p.G, hq = eh * p.G + (e0 + r) - i * p.G;
-            const float f = ll > 0.f ? 1.f / ll : 0.f;
-            const long long at = ((long long)(erow + i) * p.Hq + hq) * D + x;
-            if (p.out_f32) {
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
-                    make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-            } else {
-                const __half2 a = __floats2half2_rn(v.x * f, v.y * f), b = __floats2half2_rn(v.z * f, v.w * f);
-                *reinterpret_cast<uint2 *>(static_cast<__half *>(p.out) + at) =
-                    make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-            }
-            if (p.lse && x == 0)
-                p.lse[(long long)(erow + i) * p.Hq + hq] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-        };
+                    for (int ch = 0; ch < kChunks; ++ch)
+                        *reinterpret_cast<float2 *>(dst + ch * 16) = make_float2(o[nt][ch][e], o[nt][ch][e + 2]);
+                }
+            ok = meet();
+            if (!ok) break;
+            const int e0 = bt.rt * kRows, erows = min(kRows, bt.rows * p.G - e0), eh = bt.h, erow = bt.row;
+            const int c0 = bt.c0, c1 = bt.c1, grid = gridDim.x, me = blockIdx.x;
+            auto slot_of = [&](int cc) { return (size_t)(2 * cc + (cc == c0)); };    // a CTA begins at most one shared item
+            auto emit = [&](int r, int x, const float4 &v, float mm, float ll) {
+                const int i = (e0 + r) / p.G, hq = eh * p.G + (e0 + r) - i * p.G;
+                const float f = ll > 0.f ? 1.f / ll : 0.f;
+                const long long at = ((long long)(erow + i) * p.Hq + hq) * D + x;
+                if (p.out_f32) {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
+                        make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+                } else {
+                    const __half2 a = __floats2half2_rn(v.x * f, v.y * f), b = __floats2half2_rn(v.z * f, v.w * f);
+                    *reinterpret_cast<uint2 *>(static_cast<__half *>(p.out) + at) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+                }
+                if (p.lse && x == 0)
+                    p.lse[(long long)(erow + i) * p.Hq + hq] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            };
 #pragma unroll 1
-        for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
-            const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
-            float mm = -INFINITY;
+            for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
+                const int r = i / (D / 4), x = (i - r * (D / 4)) * 4;
+                float mm = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kGroups; ++w) mm = fmaxf(mm, mls[w * kRows + r].x);
-            const float ref = mm == -INFINITY ? 0.f : mm;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            float ll = 0.f;
+                for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, mls[w * kRows + r].x);
+                const float ref = mm == -INFINITY ? 0.f : mm;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                float ll = 0.f;
 #pragma unroll
-            for (int w = 0; w < kGroups; ++w) {
-                const float2 ml = mls[w * kRows + r];
-                const float f = at_exp2(ml.x - ref);
-                const float4 y = *reinterpret_cast<const float4 *>(os + (size_t)(w * kRows + r) * S::kOStride + x);
-                v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
-                ll += ml.y * f;
+                for (int w = 0; w < WARPS; ++w) {
+                    const float2 ml = mls[w * kRows + r];
+                    const float f = at_exp2(ml.x - ref);
+                    const float4 y = *reinterpret_cast<const float4 *>(os + (size_t)(w * kRows + r) * S::kOStride + x);
+                    v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
+                    ll += ml.y * f;
+                }
+                if (c0 == c1) {
+                    emit(r, x, v, mm, ll);
+                } else {
+                    reinterpret_cast<float4 *>(p.part)[(slot_of(me) * kRows + r) * (D / 4) + x / 4] = v;
+                    if (x == 0) p.part_ml[slot_of(me) * kRows + r] = make_float2(mm, ll);
+                }
             }
-            if (whole) {
-                emit(r, x, v, mm, ll);
-            } else {
-                reinterpret_cast<float4 *>(p.part)[((size_t)slot * kRows + r) * (D / 4) + x / 4] = v;
-                if (x == 0) p.part_ml[(size_t)slot * kRows + r] = make_float2(mm, ll);
-            }
-        }
-        if (!whole) {
-            // the last part of the item to finish joins them all
-            __threadfence();
-            asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
-            if (tid == 0) {
-                const int old = atomicAdd(p.counters + c0, 1);
-                flag[0] = old == c1 - c0;
-                if (flag[0]) p.counters[c0] = 0;
-                __threadfence();
-            }
-            asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
-            if (flag[0]) {
-                // Up to a few dozen parts of 8 rows come from L2: many loads in flight, a dependent one nowhere.
-                // First the maxima, a few lanes a row; then every output's sum over the parts, in their order.
-                constexpr int kLanes = S::kJoinLanes, kBatch = 8;
-                auto slot_of = [&](int cc) { return (size_t)(2 * cc + (cc == c0)) * kRows; };
+            // Shared items.  Parts are joined kAtSegment (or a multiple, for very many) at a time by the last of them
+            // to finish, and the segments by the last segment: from L2, many loads in flight.
+            if (c0 != c1) {
+                int seg = kAtSegment;
+                while (seg * seg < c1 - c0 + 1) seg += kAtSegment;
+                const int sc0 = c0 + (me - c0) / seg * seg, sc1 = min(c1, sc0 + seg - 1), segs = (c1 - c0) / seg + 1;
                 float *top = reinterpret_cast<float *>(mls);
-                {
-                    const int r = tid / kLanes;
-                    float mm = -INFINITY;
-                    if (r < erows) {
-#pragma unroll 4
-                        for (int cc = c0 + tid % kLanes; cc <= c1; cc += kLanes)
-                            mm = fmaxf(mm, __ldcg(p.part_ml + slot_of(cc) + r).x);
+                // counts one more of `all` in; true for the last, which then sees what the others wrote
+                auto last_of = [&](int *counter, int all) {
+                    __threadfence();
+                    bool r = meet();
+                    if (tid == 0) {
+                        flag[0] = atomicAdd(counter, 1) == all - 1;
+                        if (flag[0]) *counter = 0;
+                        __threadfence();
                     }
+                    r = meet() && r;
+                    ok = r;
+                    return r && flag[0];
+                };
+                auto join = [&](int from, int to, int by, bool final) {
+                    constexpr int kLanes = S::kJoinLanes, kBatch = 8;
+                    {
+                        const int r = tid / kLanes;
+                        float mm = -INFINITY;
+                        if (r < erows)
+                            for (int cc = from + tid % kLanes * by; cc <= to; cc += kLanes * by)
+                                mm = fmaxf(mm, __ldcg(p.part_ml + slot_of(cc) * kRows + r).x);
 #pragma unroll
-                    for (int d = kLanes / 2; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-                    if (r < erows && tid % kLanes == 0) top[r] = mm;
-                }
-                asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
+                        for (int d = kLanes / 2; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+                        if (r < erows && tid % kLanes == 0) top[r] = mm;
+                    }
+                    if (!(ok = meet())) return;
 #pragma unroll 1
-                for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
-                    const int r = i / (D / 4), x = i - r * (D / 4);
-                    const float mm = top[r], ref = mm == -INFINITY ? 0.f : mm;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float ll = 0.f;
-                    for (int cb = c0; cb <= c1; cb += kBatch) {
-                        float2 ml[kBatch];
-                        float4 y[kBatch];
+                    for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
+                        const int r = i / (D / 4), x = i - r * (D / 4);
+                        const float mm = top[r], ref = mm == -INFINITY ? 0.f : mm;
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        float ll = 0.f;
+                        for (int cb = from; cb <= to; cb += kBatch * by) {
+                            float2 ml[kBatch];
+                            float4 y[kBatch];
 #pragma unroll
-                        for (int j = 0; j < kBatch; ++j) {
-                            const size_t at = slot_of(min(cb + j, c1)) + r;
-                            ml[j] = __ldcg(p.part_ml + at);
-                            y[j] = __ldcg(reinterpret_cast<const float4 *>(p.part) + at * (D / 4) + x);
+                            for (int j = 0; j < kBatch; ++j) {
+                                const size_t at = slot_of(min(cb + j * by, to)) * kRows + r;
+                                ml[j] = __ldcg(p.part_ml + at);
+                                y[j] = __ldcg(reinterpret_cast<const float4 *>(p.part) + at * (D / 4) + x);
+                            }
+#pragma unroll
+                            for (int j = 0; j < kBatch; ++j) {
+                                const float f = cb + j * by <= to ? at_exp2(ml[j].x - ref) : 0.f;
+                                v.x += y[j].x * f; v.y += y[j].y * f; v.z += y[j].z * f; v.w += y[j].w * f;
+                                ll += ml[j].y * f;
+                            }
                         }
-#pragma unroll
-                        for (int j = 0; j < kBatch; ++j) {
-                            const float f = cb + j <= c1 ? at_exp2(ml[j].x - ref) : 0.f;
-                            v.x += y[j].x * f; v.y += y[j].y * f; v.z += y[j].z * f; v.w += y[j].w * f;
-                            ll += ml[j].y * f;
+                        if (final) {
+                            emit(r, 4 * x, v, mm, ll);
+                        } else {               // over the segment's first part; the maxima and sums once all have read
+                            reinterpret_cast<float4 *>(p.part)[(slot_of(from) * kRows + r) * (D / 4) + x] = v;
+                            if (x == 0) top[kRows + r] = ll;
                         }
                     }
-                    emit(r, 4 * x, v, mm, ll);
+                    if (!final) {
+                        if (!(ok = meet())) return;
+                        if (tid < erows) p.part_ml[slot_of(from) * kRows + tid] = make_float2(top[tid], top[kRows + tid]);
+                    }
+                };
+                if (last_of(p.counters + (sc0 == c0 ? 0 : grid) + sc0, sc1 - sc0 + 1)) {
+                    join(sc0, sc1, 1, segs == 1);
+                    if (ok && segs > 1 && last_of(p.counters + 2 * grid + c0, segs)) join(c0, c0 + (segs - 1) * seg, seg, true);
                 }
+                if (!ok) break;
             }
+            ok = meet();
+            if (!ok) break;
         }
-        asm volatile("bar.sync %0, %1;" ::"n"(kBarConsumers), "n"(32 * WARPS) : "memory");
-        t0 += n;
         if (lane == 0) mbar_arrive(pfree_a + 8 * ps);
         if (++ps == kAtPieces) {
             ps = 0;
             pparity ^= 1;
         }
     }
-    if (flag[1] && tid == 0) atomicOr(p.status, kAtStatusWait);
+    if (!ok && lane == 0) atomicOr(p.status, kAtStatusWait);
 }
 
 }  // namespace eva

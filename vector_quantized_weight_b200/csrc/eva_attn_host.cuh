@@ -26,9 +26,8 @@ struct eva_kv {
     int *counters = nullptr, *status = nullptr;
     int max_grid = 0;
     int64_t workspace_bytes = 0;
-    // attention instances: rows of 8, 16 and 32 with each warp on steps of its
-    // own, and the row-sharing one
-    struct Plan { const void *fn = nullptr; int rows = 0, stages = 0, grid = 0, threads = 0; size_t smem = 0; } plan[4];
+    // attention instances: items of 8, 16 and 32 rows
+    struct Plan { const void *fn = nullptr; int rows = 0, stages = 0, grid = 0, threads = 0; size_t smem = 0; } plan[3];
     int last_plan = 0;
     int inject_wait_rounds = 0;        // failure-detection test hook, as for the linear
 };
@@ -154,10 +153,10 @@ eva_status_t validate_kv(const eva_kv_desc *d) {
 using AttendFn = void (*)(const AttendMaps, AttendParams);
 
 // One attention instance: its shared memory and the CTAs the GPU holds at once.
-template <int D, int NT, int WR, int WARPS, bool E4M3>
+template <int D, int NT, int WARPS, int CTAS, bool E4M3>
 cudaError_t plan_attend(eva_kv *h, int i, int optin) {
-    using S = AtShape<D, NT, WR, WARPS>;
-    auto fn = eva_attend_kernel<D, NT, WR, WARPS, E4M3>;
+    using S = AtShape<D, NT, WARPS, CTAS>;
+    auto fn = eva_attend_kernel<D, NT, WARPS, CTAS, E4M3>;
     eva_kv::Plan &p = h->plan[i];
     p.fn = reinterpret_cast<const void *>(fn);
     p.rows = S::kRows;
@@ -177,15 +176,12 @@ cudaError_t plan_attend(eva_kv *h, int i, int optin) {
 template <int D, bool E4M3>
 cudaError_t plan_attends(eva_kv *h, int optin) {
     if constexpr (D <= 128) {
-        cudaError_t e = plan_attend<D, 1, 1, 4, E4M3>(h, 0, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 2, 1, 4, E4M3>(h, 1, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 4, 1, 7, E4M3>(h, 2, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 4, 7, 7, E4M3>(h, 3, optin);
+        cudaError_t e = plan_attend<D, 1, 4, 3, E4M3>(h, 0, optin);
+        if (e == cudaSuccess) e = plan_attend<D, 2, 5, 2, E4M3>(h, 1, optin);
+        if (e == cudaSuccess) e = plan_attend<D, 4, 7, 1, E4M3>(h, 2, optin);
         return e;
     } else {                             // 16 rows a warp would not fit in its registers
-        cudaError_t e = plan_attend<D, 1, 1, 7, E4M3>(h, 0, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 1, 7, 7, E4M3>(h, 3, optin);
-        return e;
+        return plan_attend<D, 1, 5, 2, E4M3>(h, 0, optin);
     }
 }
 cudaError_t plan_attends(eva_kv *h, int optin) {
@@ -208,7 +204,7 @@ eva_status_t cache_map(CUtensorMap *m, const eva_kv_desc &d, void *pages) {
         found != cudaDriverEntryPointSuccess) return EVA_ERR_CUDA;
     const cuuint64_t dims[2] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.num_pages * d.kv_heads * d.page_size};
     const cuuint64_t strides[1] = {(cuuint64_t)d.head_dim};
-    const cuuint32_t box[2] = {(cuuint32_t)std::min(d.head_dim, 128), (cuuint32_t)std::min(d.page_size, kAtStep)};
+    const cuuint32_t box[2] = {(cuuint32_t)std::min(d.head_dim, 128), (cuuint32_t)std::min(d.page_size, d.head_dim > 128 ? 16 : 32)};
     const cuuint32_t ones[2] = {1, 1};
     const CUresult r = reinterpret_cast<Encode>(fn)(
         m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pages, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -387,11 +383,11 @@ eva_status_t eva_kv_create(eva_kv_t *out, const eva_kv_desc *desc, void *k_pages
     if (e == cudaSuccess) {
         chk(dalloc(&h->part, slots * desc->head_dim * sizeof(float), &h->workspace_bytes));
         chk(dalloc(&h->part_ml, slots * sizeof(float2), &h->workspace_bytes));
-        chk(dalloc(&h->counters, h->max_grid * sizeof(int), &h->workspace_bytes));
+        chk(dalloc(&h->counters, 3 * h->max_grid * sizeof(int), &h->workspace_bytes));
         chk(dalloc(&h->status, sizeof(int), &h->workspace_bytes));
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (e == cudaSuccess) chk(cudaMemsetAsync(h->counters, 0, h->max_grid * sizeof(int), s));
+    if (e == cudaSuccess) chk(cudaMemsetAsync(h->counters, 0, 3 * h->max_grid * sizeof(int), s));
     if (e == cudaSuccess) chk(cudaMemsetAsync(h->status, 0, sizeof(int), s));
     if (e == cudaSuccess) chk(cudaStreamSynchronize(s));   // any stream may use the handle from here on
     if (e != cudaSuccess) {
@@ -490,8 +486,8 @@ eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t
     p.cap = d.softcap;
     // rows of a sequence and key head, on average (the real counts are on the device)
     const int64_t rows = (T + B - 1) / B * (int64_t)p.G;
-    int i = rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3;
-    if (!h->plan[i].fn) i = 3;
+    int i = rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
+    while (!h->plan[i].fn) --i;
     h->last_plan = i;
     const eva_kv::Plan &pl = h->plan[i];
     return cuda_status(launch_pdl(reinterpret_cast<AttendFn>(const_cast<void *>(pl.fn)), dim3(pl.grid), dim3(pl.threads),
@@ -510,7 +506,7 @@ eva_status_t eva_kv_sync_status(eva_kv_t h) {
     if (!word) return EVA_OK;
     // the next call starts clean: a CTA that gave up may have left an item's count behind
     e = cudaMemset(h->status, 0, sizeof(int));
-    if (e == cudaSuccess) e = cudaMemset(h->counters, 0, h->max_grid * sizeof(int));
+    if (e == cudaSuccess) e = cudaMemset(h->counters, 0, 3 * h->max_grid * sizeof(int));
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_status(e);
     return word & kAtStatusWait ? EVA_ERR_DEVICE_TIMEOUT : EVA_ERR_BAD_INDEX;
