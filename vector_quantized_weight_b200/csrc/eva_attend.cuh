@@ -354,7 +354,7 @@ struct AtPiece {
     int c0, c1;                        // CTAs that share the item
     int pad[2];
 };
-constexpr int kAtPieces = 4;           // handed over ahead
+constexpr int kAtPieces = 2;           // handed over ahead, with their queries (the code below knows it is two)
 constexpr int kAtSmemPerSm = 228 * 1024;
 constexpr int kAtSegment = 8;          // parts that are joined at a time
 
@@ -369,7 +369,7 @@ struct AtShape {
     static constexpr size_t kQBytes = (size_t)kRows * kQStride * 2;
     static constexpr size_t kOBytes = (size_t)WARPS * kRows * kOStride * 4;
     static constexpr size_t kMlBytes = (size_t)WARPS * kRows * 8;
-    static constexpr size_t kFixedBytes = 1024 + kQBytes + kOBytes + kMlBytes + kAtPieces * (sizeof(AtPiece) + 16) + 128;
+    static constexpr size_t kFixedBytes = 1024 + kAtPieces * kQBytes + kOBytes + kMlBytes + kAtPieces * (sizeof(AtPiece) + 16) + 128;
     static constexpr size_t kStageBytes = kStepBytes + sizeof(AtScales) + 16;
     // the ring takes what a CTA's share of the 228 KB leaves (1 KB a CTA is the system's)
     static constexpr int kRoom = (int)((kAtSmemPerSm / CTAS - 1024 - kFixedBytes) / kStageBytes);
@@ -396,11 +396,11 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
     AtScales *scales = reinterpret_cast<AtScales *>(eva_smem + skip + kStages * S::kStepBytes);
     AtPiece *pieces = reinterpret_cast<AtPiece *>(scales + kStages);
     __half *qs = reinterpret_cast<__half *>(pieces + kAtPieces);
-    float *os = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(qs) + S::kQBytes);
+    float *os = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(qs) + kAtPieces * S::kQBytes);
     float2 *mls = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(os) + S::kOBytes);
     const uint32_t full_a = (uint32_t)__cvta_generic_to_shared(reinterpret_cast<uint8_t *>(mls) + S::kMlBytes);
     const uint32_t free_a = full_a + 8 * kStages, pfull_a = free_a + 8 * kStages, pfree_a = pfull_a + 8 * kAtPieces;
-    const uint32_t meet_a = pfree_a + 8 * kAtPieces;
+    const uint32_t meet_a = pfree_a + 8 * kAtPieces, q_a = (uint32_t)__cvta_generic_to_shared(qs);
     volatile int *flag = reinterpret_cast<volatile int *>(eva_smem + (meet_a + 8 - base0));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
         const int box = split ? 16 : kStep;
         int t = 0, st = 0, ahead = 0;  // steps so far, the next one's stage, steps copied before their scales were known
         uint32_t parity = 1;           // of the free barriers: the first round passes at once
-        int ps = 0;                    // the next piece's place
+        int ps = 0, handed = 0;        // the next piece's place, pieces so far
+        int used0 = kRows, used1 = kRows;      // rows of each place's queries that may not be zeros
         uint32_t pparity = 1;
         while (ok && walk.left > 0) {
             int lo, hi, c0, c1;
@@ -507,8 +508,28 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                     q.h = walk.h;
                     q.c0 = c0;
                     q.c1 = c1;
-                    mbar_arrive(pfull_a + 8 * ps);
                 }
+                {
+                    // The queries, a row a copy; zeros behind the last one, where an earlier piece's rows (at first,
+                    // anything) would pull the references of this one's.
+                    const int r0 = walk.rt * kRows, rows = min(kRows, walk.seq.n * p.G - r0);
+                    const uint32_t bar = pfull_a + 8 * ps;
+                    const int used = ps ? used1 : used0;
+                    for (int i = rows * (D / 8) + lane; i < used * (D / 8); i += 32)
+                        *reinterpret_cast<uint4 *>(qs + ps * (S::kQBytes / 2) + i / (D / 8) * S::kQStride + i % (D / 8) * 8) =
+                            make_uint4(0, 0, 0, 0);
+                    if (rows < used) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before later copies
+                    if (ps) used1 = rows; else used0 = rows;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(rows * D * 2));
+                    __syncwarp();
+                    if (lane < rows) {
+                        const int ti = (r0 + lane) / p.G, hq = walk.h * p.G + (r0 + lane) - ti * p.G;
+                        bulk_copy_g2s(q_a + (uint32_t)(ps * S::kQBytes) + (uint32_t)(lane * S::kQStride * 2),
+                                      p.q + (walk.seq.row + ti) * p.ldq + (long long)hq * D, D * 2, bar);
+                    }
+                }
+                ++handed;
                 if (++ps == kAtPieces) {
                     ps = 0;
                     pparity ^= 1;
@@ -565,6 +586,8 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
             if (lane == 0) atomicOr(p.status, kAtStatusWait);
             for (; t < ahead; ++t)
                 if (lane == 0) mbar_arrive(full_a + 8 * t);
+            for (int i = max(0, handed - kAtPieces); i < handed; ++i)
+                mbar_wait_bounded(pfull_a + 8 * (i % kAtPieces), (i / kAtPieces) & 1, p.wait_rounds);
             for (int i = max(0, t - kStages); i < t; ++i)
                 mbar_wait_bounded(full_a + 8 * (i % kStages), (i / kStages) & 1, p.wait_rounds);
         }
@@ -580,12 +603,18 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
     // All warps of the CTA have come here (and their shared-memory writes are seen); a bounded wait like the others,
     // so that a warp that gave up leaves nobody waiting.
     uint32_t meet_parity = 0;
-    auto meet = [&]() {
+    auto come = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(meet_a);
+    };
+    auto all_here = [&]() {
         const bool r = at_wait(meet_a, meet_parity, p.wait_rounds);
         meet_parity ^= 1;
         return r;
+    };
+    auto meet = [&]() {
+        come();
+        return all_here();
     };
 
     auto addr = [&](uint32_t tile, int tok, int ch) {
@@ -600,7 +629,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
     int ps = 0, ct = warp;             // the piece's place; this warp's next step of the CTA
     int own = warp;                    // and its stage, and that stage's parity
     uint32_t pparity = 0, own_parity = 0;
-    bool ok = true;
+    bool ok = true, first = true;
     for (;;) {
         ok = at_wait(pfull_a + 8 * ps, pparity, p.wait_rounds);
         if (!ok) break;
@@ -608,17 +637,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
         const int t_end = bt.t0 + bt.n, step0 = bt.s_first - bt.t0;
         if (bt.n == 0) break;
         {
-            const int r0 = bt.rt * kRows, nrows = min(kRows, bt.rows * p.G - r0), h = bt.h;
-#pragma unroll 1
-            for (int i = tid; i < kRows * (D / 8); i += 32 * WARPS) {
-                const int r = i / (D / 8), x = i - r * (D / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < nrows) {
-                    const int ti = (r0 + r) / p.G, hq = h * p.G + (r0 + r) - ti * p.G;
-                    v = reinterpret_cast<const uint4 *>(p.q + (bt.row + ti) * p.ldq + (long long)hq * D)[x];
-                }
-                *reinterpret_cast<uint4 *>(qs + r * S::kQStride + x * 8) = v;
-            }
+            const int r0 = bt.rt * kRows, nrows = min(kRows, bt.rows * p.G - r0);
             const int pos0 = bt.len - bt.rows;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -635,9 +654,8 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
             }
             pmin = pos0 + r0 / p.G;
             pmax = pos0 + (r0 + nrows - 1) / p.G;
-            ok = meet();
-            if (!ok) break;
         }
+        const __half *qp = qs + ps * (S::kQBytes / 2);
         for (; ct < t_end; ct += WARPS) {
             const int st = own;
             if constexpr (S::kTagged) {
@@ -666,7 +684,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[nt][mt][e] = 0.f;
-#pragma unroll
+#pragma unroll(NT > 1 ? 2 : kChunks / 2)
             for (int ch = 0; ch < kChunks; ch += 2) {
                 uint32_t a[MT][2][4];  // [16 tokens][chunk][fragment]
 #pragma unroll
@@ -682,7 +700,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(qs + (nt * 8 + g) * S::kQStride + (ch + x) * 16 + 4 * c);
+                        const uint2 v = *reinterpret_cast<const uint2 *>(qp + (nt * 8 + g) * S::kQStride + (ch + x) * 16 + 4 * c);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) at_mma(z[nt][mt], a[mt][x], v.x, v.y);
                     }
@@ -693,6 +711,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
             const bool edge = tok0 + kStep - 1 > pmin || (p.window > 0 && tok0 <= pmax - p.window) || sc.sk[0] < 0.f ||
                               (MT > 1 && sc.sk[MT - 1] < 0.f);
             uint32_t pb[NT][MT][2];
+            float mx[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -718,14 +737,29 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(z[nt][0][e], z[nt][0][e + 2]);
-                    if (MT > 1) mx = fmaxf(mx, fmaxf(z[nt][MT - 1][e], z[nt][MT - 1][e + 2]));
+                    mx[nt][e] = fmaxf(z[nt][0][e], z[nt][0][e + 2]);
+                    if (MT > 1) mx[nt][e] = fmaxf(mx[nt][e], fmaxf(z[nt][MT - 1][e], z[nt][MT - 1][e + 2]));
+                }
+            }
+            bool grows = false;
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    // The reference moves only when a score passes it by 2^8 (weights stay below 256): rescaling
-                    // the sums is as much work as a step's softmax.
-                    if (__any_sync(0xffffffffu, mx > m[nt][e] + kLag)) {
-                        const float mn = fmaxf(m[nt][e], mx), f = mn == -INFINITY ? 1.f : at_exp2(m[nt][e] - mn);
+            for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], d));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grows |= mx[nt][e] > m[nt][e] + kLag;
+            // The reference moves only when a score passes it by 2^8 (weights stay below 256): rescaling the sums is as
+            // much work as a step's softmax.
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(m[nt][e], mx[nt][e]), f = mn == -INFINITY ? 1.f : at_exp2(m[nt][e] - mn);
                         l[nt][e] *= f;             // 0 for the first keys
 #pragma unroll
                         for (int ch = 0; ch < kChunks; ++ch) {
@@ -734,6 +768,11 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                         }
                         m[nt][e] = mn;
                     }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
                     const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
@@ -798,7 +837,11 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
         }
         if (!ok) break;
         {
-            // the piece's sums: the warps of different steps meet in shared memory
+            // The piece's sums: the warps of different steps meet in shared memory, once all are done with what the last
+            // piece left there.
+            if (!first) ok = all_here();
+            if (!ok) break;
+            first = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -865,12 +908,15 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 float *top = reinterpret_cast<float *>(mls);
                 // counts one more of `all` in; true for the last, which then sees what the others wrote
                 auto last_of = [&](int *counter, int all) {
-                    __threadfence();
                     bool r = meet();
                     if (tid == 0) {
-                        flag[0] = atomicAdd(counter, 1) == all - 1;
-                        if (flag[0]) *counter = 0;
-                        __threadfence();
+                        __threadfence();       // of what all warps wrote before they met
+                        const bool last = atomicAdd(counter, 1) == all - 1;
+                        if (last) {
+                            *counter = 0;
+                            __threadfence();
+                        }
+                        flag[0] = last;
                     }
                     r = meet() && r;
                     ok = r;
@@ -929,8 +975,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 }
                 if (!ok) break;
             }
-            ok = meet();
-            if (!ok) break;
+            come();
         }
         if (lane == 0) mbar_arrive(pfree_a + 8 * ps);
         if (++ps == kAtPieces) {
