@@ -64,16 +64,24 @@ struct AttendParams {
 };
 
 struct alignas(64) AttendMaps {
-    CUtensorMap k, v;                  // codes as rows of D bytes: [pages * H * page][D]
+    CUtensorMap k, v;                  // codes as rows of D bytes, [pages * H * page][D] (D = 256: [2][rows][128])
 };
 
 // ---------------------------------------------------------------- small PTX
 
-__device__ __forceinline__ void at_tma_2d(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar)
-        : "memory");
+// One copy of a map's box: rows of at most 128 bytes, or both 128-byte halves of each row, one behind the other.
+template <int D>
+__device__ __forceinline__ void at_tma(uint32_t dst, const CUtensorMap *m, int y, uint32_t bar) {
+    if constexpr (D <= 128)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(m), "r"(0), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(dst), "l"(m), "r"(0), "r"(y), "r"(0), "r"(bar)
+            : "memory");
 }
 __device__ __forceinline__ void at_ldsm(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -473,17 +481,13 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                         mbar_arrive(bar);
                     const int y0 = (pid[0] * p.H + walk.h) * page + ((s_first + s) * kStep & (page - 1));
                     const int y1 = (pid[1] * p.H + walk.h) * page;
-#pragma unroll
-                    for (int x = 0; x < D; x += 128) {     // a column half of 128 bytes is [kStep][128]
-                        const uint32_t o = dst + (uint32_t)(x * kStep), o2 = o + (uint32_t)(16 * (D < 128 ? D : 128));
-                        if (pid[0] >= 0) {
-                            at_tma_2d(o, &maps.k, x, y0, bar);
-                            at_tma_2d(o + kStep * D, &maps.v, x, y0, bar);
-                        }
-                        if (two) {
-                            at_tma_2d(o2, &maps.k, x, y1, bar);
-                            at_tma_2d(o2 + kStep * D, &maps.v, x, y1, bar);
-                        }
+                    if (pid[0] >= 0) {
+                        at_tma<D>(dst, &maps.k, y0, bar);
+                        at_tma<D>(dst + kStep * D, &maps.v, y0, bar);
+                    }
+                    if (two) {
+                        at_tma<D>(dst + 16 * D, &maps.k, y1, bar);
+                        at_tma<D>(dst + kStep * D + 16 * D, &maps.v, y1, bar);
                     }
                 };
                 look(lane, pid);
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[nt][mt][e] = 0.f;
-#pragma unroll(NT > 1 ? 2 : kChunks / 2)
+#pragma unroll
             for (int ch = 0; ch < kChunks; ch += 2) {
                 uint32_t a[MT][2][4];  // [16 tokens][chunk][fragment]
 #pragma unroll

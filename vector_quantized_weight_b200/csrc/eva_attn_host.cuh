@@ -193,7 +193,8 @@ cudaError_t plan_attends(eva_kv *h, int optin) {
     return e4 ? plan_attends<256, true>(h, optin) : plan_attends<256, false>(h, optin);
 }
 
-// The cache as rows of head_dim bytes; a box is 16 or 32 tokens of at most 128 bytes.
+// The cache as rows of head_dim bytes; a box is 16 or 32 tokens.  Rows of 256 bytes are two halves of 128, the
+// swizzle's width: a third dimension, so that one copy brings both.
 eva_status_t cache_map(CUtensorMap *m, const eva_kv_desc &d, void *pages) {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -202,12 +203,13 @@ eva_status_t cache_map(CUtensorMap *m, const eva_kv_desc &d, void *pages) {
     cudaDriverEntryPointQueryResult found;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) != cudaSuccess || !fn ||
         found != cudaDriverEntryPointSuccess) return EVA_ERR_CUDA;
-    const cuuint64_t dims[2] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.num_pages * d.kv_heads * d.page_size};
-    const cuuint64_t strides[1] = {(cuuint64_t)d.head_dim};
-    const cuuint32_t box[2] = {(cuuint32_t)std::min(d.head_dim, 128), (cuuint32_t)std::min(d.page_size, d.head_dim > 128 ? 16 : 32)};
-    const cuuint32_t ones[2] = {1, 1};
+    const bool wide = d.head_dim > 128;
+    const cuuint64_t dims[3] = {(cuuint64_t)std::min(d.head_dim, 128), (cuuint64_t)d.num_pages * d.kv_heads * d.page_size, 2};
+    const cuuint64_t strides[2] = {(cuuint64_t)d.head_dim, 128};
+    const cuuint32_t box[3] = {(cuuint32_t)dims[0], (cuuint32_t)std::min(d.page_size, wide ? 16 : 32), 2};
+    const cuuint32_t ones[3] = {1, 1, 1};
     const CUresult r = reinterpret_cast<Encode>(fn)(
-        m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pages, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        m, CU_TENSOR_MAP_DATA_TYPE_UINT8, wide ? 3 : 2, pages, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
         d.head_dim >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? EVA_OK : EVA_ERR_CUDA;
