@@ -350,7 +350,7 @@ struct AtWalk {
 // What the walking warp leaves beside a step's codes, for each 16 tokens: the
 // score's factor (negative: no token there), log2 of the value scale, and one
 // over it.
-struct AtScales {
+struct alignas(16) AtScales {
     float sk[2], lsv[2], rsv[2];
     int tag, pad;                      // the step's number in its CTA
 };
@@ -363,6 +363,7 @@ struct AtPiece {
     int pad[2];
 };
 constexpr int kAtPieces = 2;           // handed over ahead, with their queries (the code below knows it is two)
+constexpr int kAtTurn = 2;             // steps copied at a time (divides 8)
 constexpr int kAtSmemPerSm = 228 * 1024;
 constexpr int kAtSegment = 8;          // parts that are joined at a time
 
@@ -550,21 +551,30 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                         sc.rsv[i] = 1.f / v;
                     }
                     const int count = min(32, n - s0);
-                    for (int i = 0; i < count; ++i) {
-                        ok = at_wait(free_a + 8 * st, parity, p.wait_rounds);
-                        if (!ok) break;
-                        if (lane == i) {
-                            sc.tag = t;
-                            scales[st] = sc;
-                            mbar_arrive(full_a + 8 * st);
-                            if (t >= ahead) copy(s0 + i, st);
+                    // kAtTurn lanes at a time wait for their stages and fill them: one step at a time took the warp
+                    // 500 to 750 cycles each, more than all the others need for the work.
+                    for (int i = 0; i < count; i += kAtTurn) {
+                        const int mine = lane - i, turn = min(kAtTurn, count - i);
+                        bool there = true;
+                        if (mine >= 0 && mine < turn) {
+                            const bool wrap = st + mine >= kStages;
+                            const int to = wrap ? st + mine - kStages : st + mine;
+                            there = at_wait(free_a + 8 * to, wrap ? parity ^ 1 : parity, p.wait_rounds);
+                            if (there) {
+                                sc.tag = t + mine;
+                                scales[to] = sc;
+                                mbar_arrive(full_a + 8 * to);
+                                if (t + mine >= ahead) copy(s0 + lane, to);
+                            }
                         }
-                        __syncwarp();
-                        if (++st == kStages) {
-                            st = 0;
+                        ok = __all_sync(0xffffffffu, there);
+                        if (!ok) break;
+                        t += turn;
+                        st += turn;
+                        if (st >= kStages) {
+                            st -= kStages;
                             parity ^= 1;
                         }
-                        ++t;
                         if (i == 8) {
                             check(s0 + 32 + lane, pid_next);
                             scale(pid_next, sk_next, sv_next);
