@@ -176,12 +176,12 @@ cudaError_t plan_attend(eva_kv *h, int i, int optin) {
 template <int D, bool E4M3>
 cudaError_t plan_attends(eva_kv *h, int optin) {
     if constexpr (D <= 128) {
-        cudaError_t e = plan_attend<D, 1, 4, 3, E4M3>(h, 0, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 2, 5, 2, E4M3>(h, 1, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 4, 7, 1, E4M3>(h, 2, optin);
+        cudaError_t e = plan_attend<D, 1, 5, 2, E4M3>(h, 0, optin);
+        if (e == cudaSuccess) e = plan_attend<D, 2, 7, 1, E4M3>(h, 1, optin);
+        if (e == cudaSuccess) e = plan_attend<D, D < 128 ? 4 : 3, 7, 1, E4M3>(h, 2, optin);   // by registers again
         return e;
     } else {                             // 16 rows a warp would not fit in its registers
-        return plan_attend<D, 1, 5, 2, E4M3>(h, 0, optin);
+        return plan_attend<D, 1, 4, 2, E4M3>(h, 0, optin);
     }
 }
 cudaError_t plan_attends(eva_kv *h, int optin) {
