@@ -329,16 +329,17 @@ eva_status_t eva_rope_run(eva_rope_t h, const void *q, int64_t ldq, const void *
         (!d.q_heads || (wide(q, ldq, bi) && wide(q_out, ldqo, bo))) &&
         (!d.kv_heads || (wide(k, ldk, bi) && wide(k_out, ldko, bo))))
         for (lanes = 4; lanes * 16 < d.head_dim;) lanes *= 2;
-    // One token a CTA and as many heads as its lanes hold at once, until that
-    // fills the GPU; then whole tokens, four a CTA.
+    // Few tokens: one a CTA, and as many heads as its lanes hold at once, until that fills the GPU.  Then whole tokens,
+    // and as many (1 to 8) as leave three CTAs an SM: a CTA computes its tokens' sines once.
     const int groups = lanes ? kRopeThreads / lanes : kRopeThreads / 32;
-    const int64_t resident = (int64_t)h->sm_count * 4;
     p.tb = 1;
     p.hs = std::min(p.H, groups);
-    if ((int64_t)T * ((p.H + p.hs - 1) / p.hs) > resident) p.hs = p.H;
-    if (T > 4 * resident) p.tb = 4;
+    if ((int64_t)T * ((p.H + p.hs - 1) / p.hs) > (int64_t)h->sm_count * 4) {
+        p.hs = p.H;
+        while (p.tb < 8 && T >= (int64_t)h->sm_count * 6 * p.tb) p.tb *= 2;
+    }
     const dim3 grid((unsigned)((T + p.tb - 1) / p.tb), (unsigned)((p.H + p.hs - 1) / p.hs));
-    const size_t smem = (size_t)p.tb * (d.rotary_dim / 2) * sizeof(float2);
+    const size_t smem = (size_t)p.tb * (d.rotary_dim / 2) * 2 * sizeof(float) + (lanes && d.norm ? 2 * d.head_dim * sizeof(float) : 0);
     return cuda_status(launch_pdl(rope_fn(d.in_dtype, d.out_dtype, lanes), grid, dim3(kRopeThreads), smem,
                                   reinterpret_cast<cudaStream_t>(stream), 0, p));
 }
@@ -440,6 +441,9 @@ eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_t *begin
     if (!guard.ok) return EVA_ERR_CUDA;
     KvReadParams p = {};
     p.tok = kv_tokens(h, starts, begins, page_table, B, T);
+    // a warp's lookups serve up to 8 rows, once that leaves enough warps
+    p.rows = 1;
+    while (p.rows < 8 && T >= (int64_t)h->sm_count * 32 * p.rows) p.rows *= 2;
     for (int i = 0; i < 2; ++i) {
         p.pages[i] = h->pages[i];
         p.scale[i] = h->scale[i];
@@ -447,8 +451,9 @@ eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_t *begin
     p.out[0] = k_out; p.out[1] = v_out;
     p.H = h->desc.kv_heads;
     p.D = h->desc.head_dim;
+    p.log_d = p.D == 64 ? 6 : p.D == 128 ? 7 : 8;
     p.status = h->status;
-    const dim3 grid(blocks_for(T, kKvThreads / 32), 2);
+    const dim3 grid(blocks_for(T, kKvThreads / 32 * p.rows), 2);
     const bool e4 = h->desc.cache_dtype == EVA_CACHE_E4M3;
     auto fn = out_dtype == EVA_F16 ? (e4 ? eva_kv_read_kernel<__half, true> : eva_kv_read_kernel<__half, false>)
                                    : (e4 ? eva_kv_read_kernel<float, true> : eva_kv_read_kernel<float, false>);

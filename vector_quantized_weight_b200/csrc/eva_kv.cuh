@@ -12,9 +12,10 @@
 // so no code is ever NaN.
 //
 //  eva_kv_append_kernel  one CTA per (sequence's page, head, keys or values)
-//  eva_kv_read_kernel    one warp per token, keys and values
+//  eva_kv_read_kernel    one warp per token (or 8 of them), keys or values
 #pragma once
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "eva_rope.cuh"
@@ -63,7 +64,8 @@ struct KvCode<false> {
     }
     static __device__ __forceinline__ void unpack4(uint32_t w, float (&v)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i));
+        for (int i = 0; i < 4; ++i)      // 2^23 + 128 + code, exactly
+            v[i] = __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7440 + i)) - 8388736.f;
     }
 };
 template <>
@@ -95,8 +97,95 @@ struct KvAppendParams {
     int *status;
 };
 
-__device__ __forceinline__ float kv_clean(float x) {
-    return x == x ? fminf(fmaxf(x, -65504.f), 65504.f) : 0.f;
+// Eight elements as they were loaded.  clean() makes them finite (+-65504 at
+// most, 0 for a NaN), in a few integer instructions where they are already,
+// and returns the largest magnitude.
+template <typename T>
+struct KvRaw;
+template <>
+struct KvRaw<__half> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __half *p) { v = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ float clean() {
+        uint32_t *w = &v.x, odd = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) odd |= ((w[i] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;    // exponent 31
+        if (odd) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int s = 0; s < 32; s += 16) {
+                    const uint32_t e = (w[i] >> s) & 0x7fffu;
+                    if (e > 0x7c00u) w[i] &= ~(0xffffu << s);
+                    if (e == 0x7c00u) w[i] -= 1u << s;
+                }
+        }
+        __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2 *>(&w[i])));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(h[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+};
+template <>
+struct KvRaw<float> {
+    float4 v[2];
+    __device__ __forceinline__ void load(const float *p) {
+        v[0] = reinterpret_cast<const float4 *>(p)[0];
+        v[1] = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ float clean() {
+        float *x = &v[0].x, m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -65504.f), 65504.f) : 0.f;
+            m = fmaxf(m, fabsf(x[i]));
+        }
+        return m;
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const float *e = &v[0].x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = e[i];
+    }
+};
+
+// Four codes of x / scale, rounded from the IEEE quotient.  A product with the
+// reciprocal is within 2^-22 of it, so it rounds to the same code unless it
+// lies that near to a border between two codes; then, and only then, `sure`
+// becomes false (one element in some thousands) and the caller divides.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t kv_codes(const float *x, float inv, bool &sure) {
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = x[i] * inv;
+    if constexpr (E4M3) {
+        // borders: half way between neighbours, three fraction bits apart (below 2^-6 every code has the same step:
+        // left to the division)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t tail = (__float_as_uint(q[i]) & 0xfffffu) - 0x7fff8u;
+            if (tail <= 16u || (fabsf(q[i]) < 0.015626f && q[i] != 0.f)) sure = false;
+        }
+        return KvCode<true>::pack4(q[0], q[1], q[2], q[3]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float t = q[i] + 12582912.f;                 // 1.5 * 2^23: the integer lies in the low bits
+            if (fabsf(q[i] - (t - 12582912.f)) > 0.4999f) sure = false;
+            w[i] = __float_as_uint(t);
+        }
+        return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+    }
 }
 
 // The unit-th page that the call writes, counting through the sequences; every
@@ -158,46 +247,38 @@ __global__ void __launch_bounds__(kKvThreads) eva_kv_append_kernel(KvAppendParam
     const bool found = kv_find_unit(p.tok, blockIdx.x, u, bad);
     if (bad) atomicOr(p.status, kKvStatusIndex);
     if (!found) return;
+    const int h = blockIdx.y, kv = blockIdx.z, D = p.D, tid = threadIdx.x;
+    const int per = D >> 3, chunks = (u.hi - u.lo) * per;          // 8 elements a chunk
+    const long long ld = kv ? p.ld[1] : p.ld[0];
+    const TI *src = static_cast<const TI *>(kv ? p.x[1] : p.x[0]) + u.row * ld + (long long)h * D;
+    // The first chunks of a thread stay in registers between the two passes; they are on their way while the page and
+    // its scale are looked up.
+    constexpr int kKeep = sizeof(TI) == 2 ? 8 : 4;
+    KvRaw<TI> keep[kKeep];
+    float amax = 0.f;
+    auto load = [&](int c, KvRaw<TI> &r) {
+        const int t = c / per;
+        r.load(src + t * ld + (c - t * per) * 8);
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (tid + i * kKvThreads < chunks) load(tid + i * kKvThreads, keep[i]);
     const int page = p.tok.table[(long long)u.b * p.tok.max_pages + u.page_index];
     if (page < 0 || page >= p.tok.num_pages) {
         if (threadIdx.x == 0) atomicOr(p.status, kKvStatusIndex);
         return;
     }
-    const int h = blockIdx.y, kv = blockIdx.z, D = p.D, tid = threadIdx.x;
-    const int per = D >> 3, chunks = (u.hi - u.lo) * per;          // 8 elements a chunk
-    const long long ld = kv ? p.ld[1] : p.ld[0];
-    const TI *src = static_cast<const TI *>(kv ? p.x[1] : p.x[0]) + u.row * ld + (long long)h * D;
     const long long tile = (long long)page * p.H + h;
     uint8_t *dst = (kv ? p.pages[1] : p.pages[0]) + tile * p.tok.page * D;
     float *scale = (kv ? p.scale[1] : p.scale[0]) + tile;
     const float was = u.lo > 0 ? *scale : 0.f;
-    // The first chunks of a thread stay in registers between the two passes.
-    constexpr int kKeep = 4;
-    float keep[kKeep][8];
-    float amax = 0.f;
-    auto load = [&](int c, float (&v)[8]) {
-        const int t = c / per;
-        rope_load8(src + t * ld + (c - t * per) * 8, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = kv_clean(v[j]);
-    };
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-        const int c = tid + i * kKvThreads;
-        if (c >= chunks) continue;
-        load(c, keep[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-        if (tid + i * kKvThreads >= chunks) continue;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(keep[i][j]));
-    }
+    for (int i = 0; i < kKeep; ++i)
+        if (tid + i * kKvThreads < chunks) amax = fmaxf(amax, keep[i].clean());
     for (int c = tid + kKeep * kKvThreads; c < chunks; c += kKvThreads) {
-        float v[8];
-        load(c, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+        KvRaw<TI> r;
+        load(c, r);
+        amax = fmaxf(amax, r.clean());
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -221,12 +302,23 @@ __global__ void __launch_bounds__(kKvThreads) eva_kv_append_kernel(KvAppendParam
             reinterpret_cast<uint4 *>(dst)[i] = w;
         }
     }
-    auto store = [&](int c, const float (&v)[8]) {
-        float q[8];
+    const float inv = now > 0.f ? __fdiv_rn(1.f, now) : 0.f;
+    const bool usual = now > 1e-30f;     // the reciprocal is a normal number
+    auto store = [&](int c, const KvRaw<TI> &r) {
+        float x[8];
+        r.get(x);
+        bool sure = usual;
+        uint2 w;
+        w.x = kv_codes<E4M3>(x, inv, sure);
+        w.y = kv_codes<E4M3>(x + 4, inv, sure);
+        if (!sure) {
+            float q[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = now > 0.f ? __fdiv_rn(v[j], now) : 0.f;
-        *reinterpret_cast<uint2 *>(dst + (long long)u.lo * D + c * 8) =
-            make_uint2(KvCode<E4M3>::pack4(q[0], q[1], q[2], q[3]), KvCode<E4M3>::pack4(q[4], q[5], q[6], q[7]));
+            for (int j = 0; j < 8; ++j) q[j] = now > 0.f ? __fdiv_rn(x[j], now) : 0.f;
+            w.x = KvCode<E4M3>::pack4(q[0], q[1], q[2], q[3]);
+            w.y = KvCode<E4M3>::pack4(q[4], q[5], q[6], q[7]);
+        }
+        *reinterpret_cast<uint2 *>(dst + (long long)u.lo * D + c * 8) = w;
     };
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) {
@@ -234,9 +326,10 @@ __global__ void __launch_bounds__(kKvThreads) eva_kv_append_kernel(KvAppendParam
         if (c < chunks) store(c, keep[i]);
     }
     for (int c = tid + kKeep * kKvThreads; c < chunks; c += kKvThreads) {
-        float v[8];
-        load(c, v);
-        store(c, v);
+        KvRaw<TI> r;
+        load(c, r);
+        r.clean();
+        store(c, r);
     }
 }
 
@@ -245,52 +338,69 @@ struct KvReadParams {
     const uint8_t *pages[2];
     const float *scale[2];
     void *out[2];                        // [T][H][D], contiguous; either may be null
-    int H, D;
+    int H, D, log_d, rows;               // rows: of a warp, at most 8
     int *status;
 };
 
 template <typename TO, bool E4M3>
 __global__ void __launch_bounds__(kKvThreads) eva_kv_read_kernel(KvReadParams p) {
     const int lane = threadIdx.x & 31, kv = blockIdx.y;
-    const int row = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
+    const int row0 = (blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5)) * p.rows;
     pdl_wait();
     pdl_launch();
     void *dst = kv ? p.out[1] : p.out[0];
-    if (row >= p.tok.T || !dst) return;
-    // the sequence: how many of starts[1 .. B] are at or before this row
+    if (row0 >= p.tok.T || !dst) return;
+    // Lane r looks up row r of the warp.  Its sequence: how many of starts[1 .. B] are at or before it.
+    const int row = row0 + lane;
+    const bool mine = lane < p.rows && row < p.tok.T;
     int b = 0;
     for (int b0 = 1; b0 <= p.tok.B; b0 += 32) {
-        const bool le = b0 + lane <= p.tok.B && p.tok.starts[b0 + lane] <= row;
-        b += __popc(__ballot_sync(0xffffffffu, le));
+        const int at = b0 + lane <= p.tok.B ? p.tok.starts[b0 + lane] : INT_MAX;
+        for (int r = 0; r < p.rows; ++r) {
+            const int n = __popc(__ballot_sync(0xffffffffu, at <= row0 + r));
+            if (lane == r) b += n;
+        }
     }
-    if (b >= p.tok.B) return;            // behind the last sequence: left as it was
-    const int first = p.tok.starts[b], begin = p.tok.lens[b];
-    const long long pos = (long long)begin + row - first;
-    int page = -1;
-    if (first >= 0 && row >= first && begin >= 0 && pos < (long long)p.tok.max_pages * p.tok.page)
-        page = p.tok.table[(long long)b * p.tok.max_pages + pos / p.tok.page];
-    if (page < 0 || page >= p.tok.num_pages) {
-        if (lane == 0) atomicOr(p.status, kKvStatusIndex);
-        return;
+    long long tile = -1;                 // (page, head 0), -1: nothing to read
+    int slot = 0;
+    if (mine && b < p.tok.B) {           // rows behind the last sequence stay as they were
+        const int first = p.tok.starts[b], begin = p.tok.lens[b];
+        const long long pos = (long long)begin + row - first;
+        int page = -1;
+        if (first >= 0 && row >= first && begin >= 0 && pos < (long long)p.tok.max_pages * p.tok.page) {
+            page = p.tok.table[(long long)b * p.tok.max_pages + pos / p.tok.page];
+            slot = (int)(pos % p.tok.page);
+        }
+        if (page < 0 || page >= p.tok.num_pages)
+            atomicOr(p.status, kKvStatusIndex);
+        else
+            tile = (long long)page * p.H;
     }
-    const int slot = (int)(pos % p.tok.page);
-    TO *out = static_cast<TO *>(dst) + (long long)row * p.H * p.D;
     const uint8_t *pages = kv ? p.pages[1] : p.pages[0];
     const float *scale = kv ? p.scale[1] : p.scale[0];
-    for (int e = lane * 8; e < p.H * p.D; e += 256) {
-        const int h = e / p.D;
-        const long long tile = (long long)page * p.H + h;
-        const float s = scale[tile];
-        const uint2 w = *reinterpret_cast<const uint2 *>(pages + (tile * p.tok.page + slot) * p.D + e - h * p.D);
-        float v[8], a[4], c[4];
-        KvCode<E4M3>::unpack4(w.x, a);
-        KvCode<E4M3>::unpack4(w.y, c);
+    for (int r = 0; r < p.rows; ++r) {
+        const long long tr = __shfl_sync(0xffffffffu, tile, r);
+        const int sr = __shfl_sync(0xffffffffu, slot, r);
+        if (tr < 0) continue;
+        TO *out = static_cast<TO *>(dst) + (long long)(row0 + r) * p.H * p.D;
+        for (int e = lane * 16; e < p.H * p.D; e += 512) {
+            const int h = e >> p.log_d;
+            const float s = scale[tr + h];
+            const uint4 w = *reinterpret_cast<const uint4 *>(pages + (((tr + h) * p.tok.page + sr) << p.log_d) + (e & (p.D - 1)));
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = a[j] * s;
-            v[4 + j] = c[j] * s;
+            for (int i = 0; i < 2; ++i) {
+                float v[8], a[4], c[4];
+                KvCode<E4M3>::unpack4(ws[2 * i], a);
+                KvCode<E4M3>::unpack4(ws[2 * i + 1], c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = a[j] * s;
+                    v[4 + j] = c[j] * s;
+                }
+                rope_store8(out + e + 8 * i, v);
+            }
         }
-        rope_store8(out + e, v);
     }
 }
 

@@ -44,16 +44,42 @@ struct RopeParams {
     float eps, offset, magnitude;
 };
 
-// cos and sin of the tokens t0 .. t0 + nt - 1, [token][pair], by the whole CTA.
-__device__ __forceinline__ void rope_angles(const RopeParams &p, int t0, int nt, float2 *cs) {
+// cos and sin of the tokens t0 .. t0 + nt - 1, [token][pair] each, by the whole CTA.
+__device__ __forceinline__ void rope_angles(const RopeParams &p, int t0, int nt, float *cos, float *sin) {
     const int half = p.R >> 1;
     for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
         const int t = i / half, j = i - t * half;
         const unsigned long long a = (unsigned long long)(long long)p.pos[t0 + t] * p.turns[j];
         float s, c;
         sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns in [-1, 1)
-        cs[i] = make_float2(c * p.magnitude, s * p.magnitude);
+        cos[i] = c * p.magnitude;
+        sin[i] = s * p.magnitude;
     }
+}
+
+// Two fp32 operations an instruction.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ unsigned long long f2_bits(F2 a) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ F2 f2_of(unsigned long long r) {
+    F2 a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+    return a;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return f2_of(r);
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+    return f2_of(r);
 }
 
 template <typename T>
@@ -89,110 +115,170 @@ __device__ __forceinline__ void rope_store8(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// 16 elements of a lane as they were loaded: two chunks of 8.
+template <typename T>
+struct RopeRaw {
+    uint4 v[sizeof(T)];                  // 2 x 16 bytes of fp16, 4 of fp32
+    __device__ __forceinline__ void load(const T *a, const T *b) {
+        constexpr int h = sizeof(T) / 2;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            v[i] = reinterpret_cast<const uint4 *>(a)[i];
+            v[h + i] = reinterpret_cast<const uint4 *>(b)[i];
+        }
+    }
+    __device__ __forceinline__ void get(F2 (&x)[4], F2 (&y)[4]) const {
+        if constexpr (sizeof(T) == 2) {
+            const __half2 *e = reinterpret_cast<const __half2 *>(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = __half22float2(e[i]), b = __half22float2(e[4 + i]);
+                x[i] = {a.x, a.y};
+                y[i] = {b.x, b.y};
+            }
+        } else {
+            const F2 *e = reinterpret_cast<const F2 *>(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = e[i];
+                y[i] = e[4 + i];
+            }
+        }
+    }
+};
+
 // W lanes a head (a power of two >= D/16).  Needs D and R multiples of 16, and
-// every pointer and stride a multiple of 16 bytes.
+// every pointer and stride a multiple of 16 bytes.  A lane keeps the loads of its
+// next turns in flight (with one turn's, a prompt of 8192 tokens and 72 heads of
+// 128 took 86 us: 24 KB an SM are too few for the memory's latency).
 template <typename TI, typename TO, int W>
-__global__ void __launch_bounds__(kRopeThreads) eva_rope_kernel(RopeParams p) {
-    float2 *cs = reinterpret_cast<float2 *>(eva_smem);
+__global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p) {
+    constexpr int kAhead = sizeof(TI) == 2 ? 3 : 1;
+    float *ws = reinterpret_cast<float *>(eva_smem);       // weight + offset (or 1) of queries and of keys
+    float *cos = ws + (p.norm ? 2 * p.D : 0), *sin = cos + p.tb * (p.R >> 1);
     const int unit = threadIdx.x % W, group = threadIdx.x / W, groups = kRopeThreads / W;
     const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0), half = p.R >> 1;
     const bool live = unit * 16 < p.D, turned = unit * 16 < p.R;
     // the two chunks of this lane
     const bool split = turned && !p.interleaved;
     const int oa = split ? unit * 8 : unit * 16, ob = split ? half + unit * 8 : oa + 8;
+    if (p.norm)
+        for (int i = threadIdx.x; i < 2 * p.D; i += kRopeThreads) {
+            const __half *w = i < p.D ? p.qw : p.kw;
+            ws[i] = w ? __half2float(w[i < p.D ? i : i - p.D]) + p.offset : 1.f;
+        }
     pdl_wait();
     pdl_launch();
-    float wq[2][8], wk[2][8];            // weight + offset, or 1
-    if (p.norm && live) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) wq[0][i] = wq[1][i] = wk[0][i] = wk[1][i] = 1.f;
-        if (p.qw) { rope_load8(p.qw + oa, wq[0]); rope_load8(p.qw + ob, wq[1]); }
-        if (p.kw) { rope_load8(p.kw + oa, wk[0]); rope_load8(p.kw + ob, wk[1]); }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (p.qw) { wq[0][i] += p.offset; wq[1][i] += p.offset; }
-            if (p.kw) { wk[0][i] += p.offset; wk[1][i] += p.offset; }
-        }
-    }
     // (token, head) pairs of this CTA: heads [h0, h1) of each token
-    const int h0 = blockIdx.y * p.hs, nh = min(p.hs, p.H - h0);
-    float a[8], b[8];
-    auto load = [&](int i) {
-        const int t = t0 + i / nh, h = h0 + i % nh;
-        const TI *src = h < p.Hq ? static_cast<const TI *>(p.q) + t * p.ldq + (long long)h * p.D
-                                 : static_cast<const TI *>(p.k) + t * p.ldk + (long long)(h - p.Hq) * p.D;
-        if (live) {
-            rope_load8(src + oa, a);
-            rope_load8(src + ob, b);
+    const int h0 = blockIdx.y * p.hs, nh = min(p.hs, p.H - h0), n = nt * nh;
+    const float inv_d = 1.f / (float)p.D;
+    RopeRaw<TI> raw[kAhead];
+    // the pair `groups` further on, without a division a turn
+    struct At {
+        int t, h;
+    };
+    const int dt = groups / nh, dh = groups - dt * nh;
+    auto step = [&](At &a) {
+        a.t += dt;
+        a.h += dh;
+        if (a.h >= nh) {
+            a.h -= nh;
+            ++a.t;
         }
     };
-    const int n = nt * nh;
-    if (group < n) load(group);          // in flight while the angles are computed
-    rope_angles(p, t0, nt, cs);
+    At in = {group / nh, group % nh}, out = in;
+    auto load = [&](RopeRaw<TI> &r) {
+        const int t = t0 + in.t, h = h0 + in.h;
+        const bool on = in.t < nt && live;
+        step(in);
+        if (!on) return;
+        const TI *src = h < p.Hq ? static_cast<const TI *>(p.q) + t * p.ldq + (long long)h * p.D
+                                 : static_cast<const TI *>(p.k) + t * p.ldk + (long long)(h - p.Hq) * p.D;
+        r.load(src + oa, src + ob);
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) load(raw[j]);      // in flight while the angles are computed
+    rope_angles(p, t0, nt, cos, sin);
     __syncthreads();
-    // every group takes the same number of turns, so the shuffles see whole warps
-    for (int i = group, first = 1; i - group < n; i += groups, first = 0) {
-        const bool on = i < n && live;
-        if (!first && i < n) load(i);
-        const int t = i / nh, h = h0 + i % nh;
+    auto turn = [&](const RopeRaw<TI> &r) {
+        const int t = out.t, h = h0 + out.h;
+        const bool on = t < nt && live;
+        step(out);
+        F2 a[4], b[4];
+        r.get(a, b);
         if (p.norm) {
             float ss = 0.f;
             if (on) {
+                F2 q = {0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ss += a[j] * a[j] + b[j] * b[j];
+                for (int j = 0; j < 4; ++j) q = f2_fma(b[j], b[j], f2_fma(a[j], a[j], q));
+                ss = q.x + q.y;
             }
 #pragma unroll
             for (int o = W / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, W);
-            const float r = rsqrtf(ss / (float)p.D + p.eps);
-            const bool isq = h < p.Hq;
+            const float s = rsqrtf(ss * inv_d + p.eps);
+            if (on) {
+                const float *w = ws + (h < p.Hq ? 0 : p.D);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a[j] *= r * (isq ? wq[0][j] : wk[0][j]);
-                b[j] *= r * (isq ? wq[1][j] : wk[1][j]);
+                for (int j = 0; j < 2; ++j) {
+                    const float4 wa = reinterpret_cast<const float4 *>(w + oa)[j], wb = reinterpret_cast<const float4 *>(w + ob)[j];
+                    a[2 * j] = f2_mul(f2_mul(a[2 * j], {s, s}), {wa.x, wa.y});
+                    a[2 * j + 1] = f2_mul(f2_mul(a[2 * j + 1], {s, s}), {wa.z, wa.w});
+                    b[2 * j] = f2_mul(f2_mul(b[2 * j], {s, s}), {wb.x, wb.y});
+                    b[2 * j + 1] = f2_mul(f2_mul(b[2 * j + 1], {s, s}), {wb.z, wb.w});
+                }
             }
         }
-        if (!on) continue;
+        if (!on) return;
         if (turned) {
-            const float4 *row = reinterpret_cast<const float4 *>(cs + t * half + unit * 8);
-            if (!p.interleaved) {
+            const float4 *cr = reinterpret_cast<const float4 *>(cos + t * half + unit * 8);
+            const float4 *sr = reinterpret_cast<const float4 *>(sin + t * half + unit * 8);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 c = row[j];
-                    const float a0 = a[2 * j], a1 = a[2 * j + 1];
-                    a[2 * j] = a0 * c.x - b[2 * j] * c.y;
-                    b[2 * j] = b[2 * j] * c.x + a0 * c.y;
-                    a[2 * j + 1] = a1 * c.z - b[2 * j + 1] * c.w;
-                    b[2 * j + 1] = b[2 * j + 1] * c.z + a1 * c.w;
-                }
-            } else {
+            for (int j = 0; j < 2; ++j) {
+                const float4 c = cr[j], n = sr[j];
+                if (!p.interleaved) {
+                    const F2 c0 = {c.x, c.y}, c1 = {c.z, c.w}, s0 = {n.x, n.y}, s1 = {n.z, n.w};
+                    const F2 x0 = a[2 * j], x1 = a[2 * j + 1], y0 = b[2 * j], y1 = b[2 * j + 1];
+                    a[2 * j] = f2_fma(y0, {-s0.x, -s0.y}, f2_mul(x0, c0));
+                    a[2 * j + 1] = f2_fma(y1, {-s1.x, -s1.y}, f2_mul(x1, c1));
+                    b[2 * j] = f2_fma(x0, s0, f2_mul(y0, c0));
+                    b[2 * j + 1] = f2_fma(x1, s1, f2_mul(y1, c1));
+                } else {                  // four pairs of a, then four of b
+                    F2 *v = j ? b : a;
+                    const float cc[4] = {c.x, c.y, c.z, c.w}, nn[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {     // pairs of a, then pairs of b
-                    const float4 c = row[j >> 1], d = row[2 + (j >> 1)];
-                    const float ca = j & 1 ? c.z : c.x, sa = j & 1 ? c.w : c.y;
-                    const float cb = j & 1 ? d.z : d.x, sb = j & 1 ? d.w : d.y;
-                    const float a0 = a[2 * j], b0 = b[2 * j];
-                    a[2 * j] = a0 * ca - a[2 * j + 1] * sa;
-                    a[2 * j + 1] = a[2 * j + 1] * ca + a0 * sa;
-                    b[2 * j] = b0 * cb - b[2 * j + 1] * sb;
-                    b[2 * j + 1] = b[2 * j + 1] * cb + b0 * sb;
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 x = v[i];
+                        v[i] = f2_fma({x.y, x.x}, {-nn[i], nn[i]}, f2_mul(x, {cc[i], cc[i]}));
+                    }
                 }
             }
         }
         TO *dst = h < p.Hq ? static_cast<TO *>(p.qo) + (t0 + t) * p.ldqo + (long long)h * p.D
                            : static_cast<TO *>(p.ko) + (t0 + t) * p.ldko + (long long)(h - p.Hq) * p.D;
-        rope_store8(dst + oa, a);
-        rope_store8(dst + ob, b);
+        rope_store8(dst + oa, reinterpret_cast<const float(&)[8]>(a));
+        rope_store8(dst + ob, reinterpret_cast<const float(&)[8]>(b));
+    };
+    // every group takes the same number of turns, so the shuffles see whole warps
+    for (int i = 0; i < n; i += kAhead * groups) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (i + j * groups >= n) break;
+            const RopeRaw<TI> r = raw[j];
+            load(raw[j]);
+            turn(r);
+        }
     }
 }
 
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) eva_rope_any_kernel(RopeParams p) {
-    float2 *cs = reinterpret_cast<float2 *>(eva_smem);
+    float *cos = reinterpret_cast<float *>(eva_smem), *sin = cos + p.tb * (p.R >> 1);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0), half = p.R >> 1;
     pdl_wait();
     pdl_launch();
-    rope_angles(p, t0, nt, cs);
+    rope_angles(p, t0, nt, cos, sin);
     __syncthreads();
     const int h0 = blockIdx.y * p.hs, nh = min(p.hs, p.H - h0);
     for (int i = warp; i < nt * nh; i += kRopeThreads / 32) {
@@ -220,7 +306,7 @@ __global__ void __launch_bounds__(kRopeThreads) eva_rope_any_kernel(RopeParams p
         };
         for (int j = lane; j < half; j += 32) {
             const int ja = p.interleaved ? 2 * j : j, jb = p.interleaved ? 2 * j + 1 : j + half;
-            const float2 c = cs[t * half + j];
+            const float2 c = make_float2(cos[t * half + j], sin[t * half + j]);
             const float xa = scaled(ja), xb = scaled(jb);
             dst[ja] = (TO)(xa * c.x - xb * c.y);
             dst[jb] = (TO)(xb * c.x + xa * c.y);

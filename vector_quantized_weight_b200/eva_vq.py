@@ -514,10 +514,13 @@ class _OnDevice:
             raise ValueError(f"the stream is on {stream.device}, the handle on {self.device}")
         return stream.cuda_stream
 
-    def _empty(self, shape, dtype, stream):
-        import torch
+    def _empty(self, shape, dtype, stream, like):
+        """An output of the call's stream; `like`: a tensor of this device, which may have the shape and type too."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            if like.dtype == dtype:
+                return like.new_empty(shape)
+            return like.new_empty(shape, dtype=dtype)
+        import torch
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
@@ -583,13 +586,13 @@ class HeadRope(_OnDevice):
         if self.rotary_dim or positions is not None:
             _indices("positions", positions, (T,), dev)
         if q_out is None:
-            q_out, ldqo = self._empty((T, Hq, D), self.out_dtype, stream), Hq * D
+            q_out, ldqo = self._empty((T, Hq, D), self.out_dtype, stream, q), Hq * D
         else:
             To, ldqo = _rows("q_out", q_out, Hq, D, self.out_dtype, dev)
             if To != T:
                 raise ValueError(f"q_out has {To} rows, q has {T}")
         if k_out is None:
-            k_out, ldko = self._empty((T, Hk, D), self.out_dtype, stream), Hk * D
+            k_out, ldko = self._empty((T, Hk, D), self.out_dtype, stream, k), Hk * D
         else:
             To, ldko = _rows("k_out", k_out, Hk, D, self.out_dtype, dev)
             if To != T:
@@ -692,7 +695,7 @@ class KVCache(_OnDevice):
         Hq, D, dev = self.q_heads, self.head_dim, self.device
         T, ldq = _rows("q", q, Hq, D, torch.float16, dev)
         if out is None:
-            out = self._empty((T, Hq, D), self.out_dtype, stream)
+            out = self._empty((T, Hq, D), self.out_dtype, stream, q)
         elif _rows("out", out, Hq, D, self.out_dtype, dev) != (T, Hq * D):
             raise ValueError(f"out must be a contiguous [{T}][{Hq}][{D}] tensor")
         if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != (T, Hq) or
@@ -713,7 +716,7 @@ class KVCache(_OnDevice):
         outs = []
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is None:
-                t = self._empty(shape, dtype, stream)
+                t = self._empty(shape, dtype, stream, self.k_scale)
             elif t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}")
             outs.append(t)
