@@ -453,8 +453,8 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                     id[0] = id[1] = -1;
                     if (s >= n) return;
                     const int tok0 = (s_first + s) * kStep;
-                    if (tok0 < walk.seq.len) id[0] = table[tok0 / page];
-                    if (MT > 1 && tok0 + 16 < walk.seq.len) id[1] = split ? table[tok0 / page + 1] : id[0];
+                    if (tok0 < walk.seq.len) id[0] = table[tok0 >> p.tok.log_page];
+                    if (MT > 1 && tok0 + 16 < walk.seq.len) id[1] = split ? table[(tok0 >> p.tok.log_page) + 1] : id[0];
                 };
                 auto check = [&](int s, int (&id)[2]) {    // a page outside the cache: no token there, and say so
 #pragma unroll

@@ -10,6 +10,7 @@
 struct eva_rope {
     eva_rope_desc desc;
     int device = 0, sm_count = 0;
+    void *memory = nullptr;                // what follows
     unsigned long long *turns = nullptr;   // [rotary_dim / 2]
     __half *w[2] = {nullptr, nullptr};     // norm weights of queries and keys
     float magnitude = 1.f;
@@ -21,9 +22,10 @@ struct eva_kv {
     uint8_t *pages[2] = {nullptr, nullptr};   // the caller's
     float *scale[2] = {nullptr, nullptr};
     AttendMaps maps;
+    uint8_t *memory = nullptr;             // what follows; the counters and the status word first
+    int *counters = nullptr, *status = nullptr;
     float *part = nullptr;
     float2 *part_ml = nullptr;
-    int *counters = nullptr, *status = nullptr;
     int max_grid = 0;
     int64_t workspace_bytes = 0;
     // attention instances: items of 8, 16 and 32 rows
@@ -50,10 +52,15 @@ struct DeviceGuard {
     }
 };
 
-eva_status_t sm100_device(int *dev, cudaDeviceProp *prop) {
-    if (cudaGetDevice(dev) != cudaSuccess) return EVA_ERR_NO_DEVICE;
-    if (cudaGetDeviceProperties(prop, *dev) != cudaSuccess) return EVA_ERR_NO_DEVICE;
-    return prop->major == 10 ? EVA_OK : EVA_ERR_NO_DEVICE;
+// The current device, its SMs and the shared memory a block may have; attributes, as the whole property structure takes
+// most of a millisecond.
+eva_status_t sm100_device(int *dev, int *sms, int *optin) {
+    int major = 0;
+    if (cudaGetDevice(dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, *dev) != cudaSuccess) return EVA_ERR_NO_DEVICE;
+    return major == 10 ? EVA_OK : EVA_ERR_NO_DEVICE;
 }
 
 bool valid_dtype(eva_dtype_t t) { return t == EVA_F16 || t == EVA_F32; }
@@ -218,24 +225,26 @@ eva_status_t cache_map(CUtensorMap *m, const eva_kv_desc &d, void *pages) {
 void free_rope(eva_rope *h) {
     if (!h) return;
     DeviceGuard guard(h->device);
-    void *ptrs[] = {h->turns, h->w[0], h->w[1]};
-    for (void *p : ptrs)
-        if (p) cudaFree(p);
+    if (h->memory) cudaFree(h->memory);
     delete h;
 }
 
 void free_kv(eva_kv *h) {
     if (!h) return;
     DeviceGuard guard(h->device);
-    void *ptrs[] = {h->part, h->part_ml, h->counters, h->status};
-    for (void *p : ptrs)
-        if (p) cudaFree(p);
+    if (h->memory) cudaFree(h->memory);
     delete h;
 }
 
 // Packed inputs and outputs: non-negative counts, 16-byte rows.
 bool row_ok(const void *p, int64_t ld, int64_t least, int bytes) {
     return p && aligned16(p) && ld >= least && ld * bytes % 16 == 0;
+}
+
+int log2_of(int pow2) {
+    int l = 0;
+    while (pow2 >> (l + 1)) ++l;
+    return l;
 }
 
 KvTokens kv_tokens(const eva_kv *h, const int32_t *starts, const int32_t *lens, const int32_t *table, int B, int T) {
@@ -246,6 +255,7 @@ KvTokens kv_tokens(const eva_kv *h, const int32_t *starts, const int32_t *lens, 
     t.B = B;
     t.T = T;
     t.page = h->desc.page_size;
+    t.log_page = log2_of(t.page);
     t.max_pages = h->desc.max_pages;
     t.num_pages = h->desc.num_pages;
     return t;
@@ -267,29 +277,33 @@ eva_status_t eva_rope_create(eva_rope_t *out, const eva_rope_desc *desc, const v
     if (st != EVA_OK) return st;
     if (!desc->norm && (q_weight || k_weight)) return EVA_ERR_INVALID_ARG;
     if (!aligned16(q_weight) || !aligned16(k_weight)) return EVA_ERR_INVALID_ARG;
-    int dev = 0;
-    cudaDeviceProp prop;
-    st = sm100_device(&dev, &prop);
+    int dev = 0, sms = 0, optin = 0;
+    st = sm100_device(&dev, &sms, &optin);
     if (st != EVA_OK) return st;
     eva_rope *h = new (std::nothrow) eva_rope();
     if (!h) return EVA_ERR_OOM;
     h->desc = *desc;
     h->device = dev;
-    h->sm_count = prop.multiProcessorCount;
+    h->sm_count = sms;
     if (desc->magnitude > 0) h->magnitude = (float)desc->magnitude;
     else if (desc->scaling == EVA_ROPE_YARN && desc->factor > 1) h->magnitude = (float)(0.1 * std::log(desc->factor) + 1.0);
     unsigned long long turns[512];
     const int pairs = desc->rotary_dim / 2;
     for (int i = 0; i < pairs; ++i) turns[i] = rope_turns(rope_frequency(*desc, i));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = dalloc(&h->turns, pairs * sizeof(turns[0]), nullptr);
-    if (e == cudaSuccess && pairs)
+    const size_t table = (pairs * sizeof(turns[0]) + 15) / 16 * 16, weight = ((size_t)desc->head_dim * sizeof(__half) + 15) / 16 * 16;
+    uint8_t *m = nullptr;
+    cudaError_t e = dalloc(&m, table + 2 * weight, nullptr);
+    h->memory = m;
+    if (e == cudaSuccess && pairs) {
+        h->turns = reinterpret_cast<unsigned long long *>(m);
         e = cudaMemcpyAsync(h->turns, turns, pairs * sizeof(turns[0]), cudaMemcpyHostToDevice, s);
+    }
     const void *w[2] = {q_weight, k_weight};
     for (int i = 0; i < 2; ++i) {
-        if (e == cudaSuccess && w[i]) e = dalloc(&h->w[i], desc->head_dim * sizeof(__half), nullptr);
-        if (e == cudaSuccess && w[i])
-            e = cudaMemcpyAsync(h->w[i], w[i], desc->head_dim * sizeof(__half), cudaMemcpyDeviceToDevice, s);
+        if (e != cudaSuccess || !w[i]) continue;
+        h->w[i] = reinterpret_cast<__half *>(m + table + i * weight);
+        e = cudaMemcpyAsync(h->w[i], w[i], desc->head_dim * sizeof(__half), cudaMemcpyDeviceToDevice, s);
     }
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);   // the table is this call's stack; the weights may go
     if (e != cudaSuccess) {
@@ -357,15 +371,14 @@ eva_status_t eva_kv_create(eva_kv_t *out, const eva_kv_desc *desc, void *k_pages
     if (st != EVA_OK) return st;
     if (!k_pages || !v_pages || !k_scale || !v_scale || !aligned16(k_pages) || !aligned16(v_pages) ||
         !aligned16(k_scale) || !aligned16(v_scale)) return EVA_ERR_INVALID_ARG;
-    int dev = 0;
-    cudaDeviceProp prop;
-    st = sm100_device(&dev, &prop);
+    int dev = 0, sms = 0, optin = 0;
+    st = sm100_device(&dev, &sms, &optin);
     if (st != EVA_OK) return st;
     eva_kv *h = new (std::nothrow) eva_kv();
     if (!h) return EVA_ERR_OOM;
     h->desc = *desc;
     h->device = dev;
-    h->sm_count = prop.multiProcessorCount;
+    h->sm_count = sms;
     h->pages[0] = static_cast<uint8_t *>(k_pages);
     h->pages[1] = static_cast<uint8_t *>(v_pages);
     h->scale[0] = k_scale;
@@ -376,22 +389,24 @@ eva_status_t eva_kv_create(eva_kv_t *out, const eva_kv_desc *desc, void *k_pages
         free_kv(h);
         return st;
     }
-    cudaError_t e = plan_attends(h, (int)prop.sharedMemPerBlockOptin);
+    cudaError_t e = plan_attends(h, optin);
     size_t slots = 0;
     for (const auto &p : h->plan) {
         slots = std::max(slots, (size_t)2 * p.grid * p.rows);
         h->max_grid = std::max(h->max_grid, p.grid);
     }
     auto chk = [&](cudaError_t r) { if (e == cudaSuccess) e = r; };
-    if (e == cudaSuccess) {
-        chk(dalloc(&h->part, slots * desc->head_dim * sizeof(float), &h->workspace_bytes));
-        chk(dalloc(&h->part_ml, slots * sizeof(float2), &h->workspace_bytes));
-        chk(dalloc(&h->counters, 3 * h->max_grid * sizeof(int), &h->workspace_bytes));
-        chk(dalloc(&h->status, sizeof(int), &h->workspace_bytes));
-    }
+    const size_t words = ((size_t)(3 * h->max_grid + 1) * sizeof(int) + 255) / 256 * 256;
+    const size_t outs = slots * desc->head_dim * sizeof(float);
+    if (e == cudaSuccess) chk(dalloc(&h->memory, words + outs + slots * sizeof(float2), &h->workspace_bytes));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (e == cudaSuccess) chk(cudaMemsetAsync(h->counters, 0, 3 * h->max_grid * sizeof(int), s));
-    if (e == cudaSuccess) chk(cudaMemsetAsync(h->status, 0, sizeof(int), s));
+    if (e == cudaSuccess) {
+        h->counters = reinterpret_cast<int *>(h->memory);
+        h->status = h->counters + 3 * h->max_grid;
+        h->part = reinterpret_cast<float *>(h->memory + words);
+        h->part_ml = reinterpret_cast<float2 *>(h->memory + words + outs);
+        chk(cudaMemsetAsync(h->memory, 0, words, s));
+    }
     if (e == cudaSuccess) chk(cudaStreamSynchronize(s));   // any stream may use the handle from here on
     if (e != cudaSuccess) {
         free_kv(h);
@@ -422,6 +437,7 @@ eva_status_t eva_kv_append(eva_kv_t h, const void *k, int64_t ldk, const void *v
     }
     p.H = d.kv_heads;
     p.D = d.head_dim;
+    p.log_d = log2_of(p.D);
     p.status = h->status;
     // n tokens lie on at most n / page + 2 pages, and on at most n
     const int64_t units = std::min<int64_t>(T, T / d.page_size + 2 * (int64_t)B);
@@ -451,7 +467,7 @@ eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_t *begin
     p.out[0] = k_out; p.out[1] = v_out;
     p.H = h->desc.kv_heads;
     p.D = h->desc.head_dim;
-    p.log_d = p.D == 64 ? 6 : p.D == 128 ? 7 : 8;
+    p.log_d = log2_of(p.D);
     p.status = h->status;
     const dim3 grid(blocks_for(T, kKvThreads / 32 * p.rows), 2);
     const bool e4 = h->desc.cache_dtype == EVA_CACHE_E4M3;

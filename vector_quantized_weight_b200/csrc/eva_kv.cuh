@@ -29,7 +29,7 @@ constexpr int kKvStatusIndex = 8;      // status bit: an index on the device was
 // packed inputs belong to sequence b; lens[b] is its length with them.
 struct KvTokens {
     const int32_t *starts, *lens, *table;
-    int B, T, page, max_pages, num_pages;
+    int B, T, page, log_page, max_pages, num_pages;
 };
 
 // Rows of sequence b and its length; a sequence whose numbers cannot be right
@@ -93,7 +93,7 @@ struct KvAppendParams {
     long long ld[2];
     uint8_t *pages[2];
     float *scale[2];
-    int H, D;
+    int H, D, log_d;
     int *status;
 };
 
@@ -206,8 +206,8 @@ __device__ __forceinline__ bool kv_find_unit(const KvTokens &k, int unit, KvUnit
             begin = max(0, s.len - s.n);
             row = s.row + s.n - (end - begin);
             if (s.n > 0 && end > begin) {
-                first = begin / k.page;
-                count = (end - 1) / k.page - first + 1;
+                first = begin >> k.log_page;
+                count = ((end - 1) >> k.log_page) - first + 1;
             }
         }
         int sum = count;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kKvThreads) eva_kv_append_kernel(KvAppendParam
     if (bad) atomicOr(p.status, kKvStatusIndex);
     if (!found) return;
     const int h = blockIdx.y, kv = blockIdx.z, D = p.D, tid = threadIdx.x;
-    const int per = D >> 3, chunks = (u.hi - u.lo) * per;          // 8 elements a chunk
+    const int log_per = p.log_d - 3, chunks = (u.hi - u.lo) << log_per;          // 8 elements a chunk
     const long long ld = kv ? p.ld[1] : p.ld[0];
     const TI *src = static_cast<const TI *>(kv ? p.x[1] : p.x[0]) + u.row * ld + (long long)h * D;
     // The first chunks of a thread stay in registers between the two passes; they are on their way while the page and
@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(kKvThreads) eva_kv_append_kernel(KvAppendParam
     KvRaw<TI> keep[kKeep];
     float amax = 0.f;
     auto load = [&](int c, KvRaw<TI> &r) {
-        const int t = c / per;
-        r.load(src + t * ld + (c - t * per) * 8);
+        const int t = c >> log_per;
+        r.load(src + t * ld + (c - (t << log_per)) * 8);
     };
 #pragma unroll
     for (int i = 0; i < kKeep; ++i)
@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(kKvThreads) eva_kv_read_kernel(KvReadParams p)
         const long long pos = (long long)begin + row - first;
         int page = -1;
         if (first >= 0 && row >= first && begin >= 0 && pos < (long long)p.tok.max_pages * p.tok.page) {
-            page = p.tok.table[(long long)b * p.tok.max_pages + pos / p.tok.page];
-            slot = (int)(pos % p.tok.page);
+            page = p.tok.table[(long long)b * p.tok.max_pages + (pos >> p.tok.log_page)];
+            slot = (int)(pos & (p.tok.page - 1));
         }
         if (page < 0 || page >= p.tok.num_pages)
             atomicOr(p.status, kKvStatusIndex);

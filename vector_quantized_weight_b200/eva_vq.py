@@ -514,15 +514,17 @@ class _OnDevice:
             raise ValueError(f"the stream is on {stream.device}, the handle on {self.device}")
         return stream.cuda_stream
 
-    def _empty(self, shape, dtype, stream, like):
-        """An output of the call's stream; `like`: a tensor of this device, which may have the shape and type too."""
-        if stream is None:
-            if like.dtype == dtype:
-                return like.new_empty(shape)
-            return like.new_empty(shape, dtype=dtype)
+    def _empty(self, shape, dtype, stream):
+        """An output that belongs to the call's stream."""
         import torch
+        if stream is None:
+            return self._like[dtype].new_empty(shape)       # cheaper than torch.empty with a type and a device
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _prototypes(self):
+        import torch
+        self._like = {d: torch.empty(0, dtype=d, device=self.device) for d in (torch.float16, torch.float32)}
 
     def __del__(self):
         try:
@@ -574,6 +576,7 @@ class HeadRope(_OnDevice):
         with torch.cuda.device(self.device):
             self.handle = eva_rope_create(self.desc, _ptr(q_weight), _ptr(k_weight), self._stream(stream))
         self._run = load().eva_rope_run
+        self._prototypes()
 
     def __call__(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """(q_out, k_out) of q [T][q_heads][head_dim], k [T][kv_heads][head_dim] (rows may lie apart, as columns of
@@ -586,13 +589,13 @@ class HeadRope(_OnDevice):
         if self.rotary_dim or positions is not None:
             _indices("positions", positions, (T,), dev)
         if q_out is None:
-            q_out, ldqo = self._empty((T, Hq, D), self.out_dtype, stream, q), Hq * D
+            q_out, ldqo = self._empty((T, Hq, D), self.out_dtype, stream), Hq * D
         else:
             To, ldqo = _rows("q_out", q_out, Hq, D, self.out_dtype, dev)
             if To != T:
                 raise ValueError(f"q_out has {To} rows, q has {T}")
         if k_out is None:
-            k_out, ldko = self._empty((T, Hk, D), self.out_dtype, stream, k), Hk * D
+            k_out, ldko = self._empty((T, Hk, D), self.out_dtype, stream), Hk * D
         else:
             To, ldko = _rows("k_out", k_out, Hk, D, self.out_dtype, dev)
             if To != T:
@@ -654,6 +657,7 @@ class KVCache(_OnDevice):
         with torch.cuda.device(self.device):
             self.handle = eva_kv_create(self.desc, *map(_ptr, made), self._stream(stream))
         lib = load()
+        self._prototypes()
         self._append, self._attend, self._read = lib.eva_kv_append, lib.eva_kv_attend, lib.eva_kv_read
 
     def clone(self, **changes):
@@ -695,7 +699,7 @@ class KVCache(_OnDevice):
         Hq, D, dev = self.q_heads, self.head_dim, self.device
         T, ldq = _rows("q", q, Hq, D, torch.float16, dev)
         if out is None:
-            out = self._empty((T, Hq, D), self.out_dtype, stream, q)
+            out = self._empty((T, Hq, D), self.out_dtype, stream)
         elif _rows("out", out, Hq, D, self.out_dtype, dev) != (T, Hq * D):
             raise ValueError(f"out must be a contiguous [{T}][{Hq}][{D}] tensor")
         if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != (T, Hq) or
@@ -716,7 +720,7 @@ class KVCache(_OnDevice):
         outs = []
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is None:
-                t = self._empty(shape, dtype, stream, self.k_scale)
+                t = self._empty(shape, dtype, stream)
             elif t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}")
             outs.append(t)
