@@ -77,6 +77,9 @@ def parse_args():
     ap.add_argument("--no-cpu", action="store_true", help="skip the oracle CPU baseline")
     ap.add_argument("--no-block", action="store_true",
                     help="skip the Llama-2-7B decoder-block leg (seven linears with their dependencies)")
+    ap.add_argument("--block-context", type=int, default=0,
+                    help="cached tokens a sequence of the decoder-block leg; > 0 puts rotary positions, the 8-bit cache "
+                         "and attention between a block's q, k, v and its o (0: o reads q's output)")
     ap.add_argument("--no-e2e", action="store_true", help="skip the host-buffer end-to-end leg")
     ap.add_argument("--cpu-seconds", type=float, default=10.0)
     ap.add_argument("--group", type=int, default=3,
@@ -489,6 +492,26 @@ def main():
                                 for li, sh in enumerate(bsh)])
                 bys.append([torch.zeros((B, sh.N), dtype=torch.float16, device=dev) for sh in bsh])
             bys[-1][6].copy_(torch.from_numpy(synth.make_x(bsh[6].N, B, seed)).to(dev))
+            # With --block-context: B sequences of that many cached tokens (random codes), a cache for each block; a
+            # step writes its tokens at the same positions every time.
+            context, heads, page = args.block_context, bsh[0].N // 128, 64
+            caches, attended = [], []
+            if context > 0:
+                pages = -(-context // page)
+                rope = eva_vq.HeadRope(heads, heads, 128)
+                gen = torch.Generator(device=dev)
+                gen.manual_seed(seed)
+                for b in range(nblk):
+                    kv = [torch.randint(-127, 128, (B * pages, heads, page, 128), generator=gen, dtype=torch.int8,
+                                        device=dev) for _ in range(2)]
+                    ks = [torch.full((B * pages, heads), 0.01, device=dev) for _ in range(2)]
+                    caches.append(eva_vq.KVCache(heads, heads, 128, num_pages=B * pages, max_seqs=B, max_pages=pages,
+                                                 page_size=page, k=kv[0], v=kv[1], k_scale=ks[0], v_scale=ks[1]))
+                    attended.append([torch.empty((B, heads, 128), dtype=torch.float16, device=dev) for _ in range(3)])
+                starts = torch.arange(B + 1, dtype=torch.int32, device=dev)
+                lens = torch.full((B,), context, dtype=torch.int32, device=dev)
+                positions = lens - 1
+                table = torch.randperm(B * pages, generator=gen, device=dev).to(torch.int32).view(B, pages)
         torch.cuda.synchronize(dev)
 
         def emit_blocks(n, start):
@@ -496,7 +519,13 @@ def main():
                 b = (start + i) % nblk
                 L, Y, xin = blayers[b], bys[b], bys[(b - 1) % nblk][6]
                 eva_vq.run_group(L[0:3], [xin] * 3, Y[0:3], stream=stream)
-                L[3](Y[0], out=Y[3], stream=stream)
+                oin = Y[0]
+                if caches:
+                    qo, ko, at = attended[b]
+                    rope(Y[0], Y[1], positions, q_out=qo, k_out=ko, stream=stream)
+                    caches[b].append(ko, Y[2], starts, lens, table, stream=stream)
+                    oin = caches[b].attend(qo, starts, lens, table, out=at, stream=stream).view(B, heads * 128)
+                L[3](oin, out=Y[3], stream=stream)
                 eva_vq.run_group(L[4:6], [Y[3]] * 2, Y[4:6], stream=stream)
                 L[6](Y[4], out=Y[6], stream=stream)
 
@@ -505,19 +534,24 @@ def main():
         torch.cuda.synchronize(dev)
         n_blocks = nblk * max(10, min(steps, 200_000) // (7 * nblk))
         ms_blk, _ = timed_units(emit_blocks, n_blocks, nblk, 1)
-        bbytes = sum(stream_bytes(sh, B) for sh in bsh)
+        bbytes = sum(stream_bytes(sh, B) for sh in bsh) + 2 * B * context * heads * 128
         us_blk = ms_blk * 1e3 / n_blocks
         block = {"us_per_block": round(us_blk, 3), "us_per_layer": round(us_blk / len(bsh), 4),
-                 "blocks": n_blocks, "ring_blocks": nblk, "launches_per_block": 4,
+                 "blocks": n_blocks, "ring_blocks": nblk, "launches_per_block": 7 if caches else 4,
+                 **({"context": context} if caches else {}),
                  "value": round(job_throughput_gbs(world, n_blocks, bbytes, ms_blk), 4), "unit": "GB/s",
                  "algorithmic_bytes_per_block": bbytes,
                  "grids": [lay.info().grid for lay in blayers[0]],
                  "note": ("Llama-2-7B decoder block, B=%d: q,k,v (one run_group) -> o -> gate,up (one run_group) "
-                          "-> down, each launch waiting for the one before it and reading its output" % B)}
+                          "-> down, each launch waiting for the one before it and reading its output" % B
+                          + ("; rotary positions, cache write and attention over %d cached tokens a sequence before o"
+                             % context if caches else ""))}
         for row in blayers:
             for lay in row:
                 lay.close()
-        del blayers, bys
+        for c in caches:
+            c.close()
+        del blayers, bys, caches
 
     # End to end through the public host-buffer call: x copied in from
     # pinned memory and y read back every step.
