@@ -476,7 +476,7 @@ typedef struct eva_kv *eva_kv_t;
 /*
  * A cache over caller-owned device buffers (16-byte aligned):
  *   k_pages, v_pages  codes [num_pages][kv_heads][page_size][head_dim], one byte each
- *   k_scale, v_scale  fp32 [num_pages][kv_heads]
+ *   k_scale, v_scale  fp32 [num_pages][kv_heads], not negative
  * They keep their contents and must live as long as the handle.  The handle owns
  * the workspace of eva_kv_attend.  Waits for `stream`.
  */
@@ -526,7 +526,7 @@ EVA_API eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_
  * to the next, rows 16-byte aligned); out [T][q_heads][head_dim] of the descriptor's out_dtype,
  * contiguous; lse (optional) fp32 [T][q_heads], the natural logarithm of the sum of
  * exponentials.  The row at position p sees keys j <= p, with a window j > p - window.  A row that
- * sees no key gives zeros and lse = -infinity.  Statistics and sums are fp32; the
+ * sees no key gives zeros and lse = -infinity; what the buffers hold where no token is does not matter.  Statistics and sums are fp32; the
  * softmax weights are rounded to fp16 for the value product.  Results do not depend
  * on timing; they may differ in the last bits between batches, whose work is
  * cut at other places.  The handle's workspace is shared: one handle must not attend on two

@@ -387,6 +387,79 @@ def test_captured_step_follows_the_device_arrays_and_other_streams():
     c.close()
 
 
+def test_refusals():
+    """What the entry points refuse with a handle in hand, before any launch."""
+    D, H = 64, 2
+    c, table = make_cache("int8", [40], 32, H, D, 81, Hq=4)
+    q = torch.zeros((1, 4, D), dtype=torch.float16, device="cuda")
+    k = torch.zeros((1, H, D), dtype=torch.float16, device="cuda")
+    s, n, t = i32([0, 1]), i32([40]), i32(table)
+    bad = [lambda: c.attend(q.float(), s, n, t), lambda: c.attend(q[:, :2], s, n, t), lambda: c.attend(q.cpu(), s, n, t),
+           lambda: c.attend(q, s.long(), n, t), lambda: c.attend(q, s, n, t[:, :1]), lambda: c.attend(q, s[:1], n, t),
+           lambda: c.attend(q, i32([0, 1, 1]), i32([40, 1]), i32(np.tile(table, (2, 1)))),      # more sequences than planned
+           lambda: c.attend(q, s, n, t, out=torch.zeros((1, 4, D), device="cuda")),
+           lambda: c.attend(q, s, n, t, lse=torch.zeros((1, 3), device="cuda")),
+           lambda: c.append(k, k.float(), s, n, t), lambda: c.append(k.bfloat16(), k.bfloat16(), s, n, t),
+           lambda: c.append(k, k[:0], s, n, t), lambda: c.append(k.transpose(1, 2), k, s, n, t),
+           lambda: c.read(s, n, t, 1, k_out=k.float()),
+           lambda: eva_vq.KVCache(4, H, D, num_pages=1, max_seqs=1, max_pages=1, k=c.k),
+           lambda: eva_vq.HeadRope(1, 1, D, norm=True, q_weight=torch.ones(D, device="cuda"))]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    rope = eva_vq.HeadRope(4, H, D)
+    for call in (lambda: rope(q, k[:0], i32([0])), lambda: rope(q, k, i32([0, 1])), lambda: rope(q, k, None)):
+        with pytest.raises(ValueError):
+            call()
+    wide = torch.zeros((3, 4 * D + 4), dtype=torch.float16, device="cuda")
+    rows = wide[:, :4 * D].unflatten(1, (4, D))                        # rows 8 bytes off a 16-byte border
+    for call in (lambda: c.attend(rows, i32([0, 3]), n, t), lambda: c.append(rows[:, :H], rows[:, :H], i32([0, 3]), n, t)):
+        with pytest.raises(eva_vq.EvaError):
+            call()
+    lib = eva_vq.load()
+    P = q.data_ptr()
+    assert lib.eva_kv_attend(c.handle, P, 4 * D - 8, P, P, P, 1, 1, P, None, None) == eva_vq.EVA_ERR_INVALID_ARG
+    assert lib.eva_kv_attend(c.handle, P, 4 * D, P, P, P, 1, 1 << 30, P, None, None) == eva_vq.EVA_ERR_UNSUPPORTED
+    assert lib.eva_kv_attend(c.handle, P, 4 * D, P, P, P, 0, 1, P, None, None) == eva_vq.EVA_ERR_INVALID_ARG
+    assert lib.eva_kv_append(c.handle, P, H * D, P, H * D, 5, P, P, P, 1, 1, None) == eva_vq.EVA_ERR_INVALID_ARG
+    assert lib.eva_kv_read(c.handle, P, P, P, 1, 1, 0, None, None, None) == eva_vq.EVA_ERR_INVALID_ARG
+    assert lib.eva_rope_run(rope.handle, P, 4 * D - 1, P, H * D, P, 1, P, 4 * D, P, H * D, None) == eva_vq.EVA_ERR_INVALID_ARG
+    assert lib.eva_rope_run(rope.handle, P, 4 * D, P, H * D, None, 1, P, 4 * D, P, H * D, None) == eva_vq.EVA_ERR_INVALID_ARG
+    assert c.status() == eva_vq.EVA_OK
+    # nothing to do is not an error
+    assert c.attend(q[:0], i32([0, 0]), n, t).shape == (0, 4, D)
+    c.append(k[:0], k[:0], i32([0, 0]), n, t)
+    assert c.read(i32([0, 0]), i32([0]), t, 0)[0].shape == (0, H, D)
+    rope.close()
+    c.close()
+    with pytest.raises(eva_vq.EvaError):
+        c.attend(q, s, n, t)
+
+
+def test_two_handles_at_once_and_a_shared_prefix():
+    """Two sequences whose tables name the same pages, read by two handles on two streams at the same time, many
+    times over."""
+    H, D, P = 4, 128, 32
+    lens = [700, 700]
+    c, table = make_cache("int8", lens, P, H, D, 91, Hq=16)
+    table[1, :20] = table[0, :20]
+    q = cuda(rng(92).standard_normal((2, 16, D)), torch.float16)
+    args = (q, i32([0, 1, 2]), i32(lens), i32(table))
+    want, _, bound = ref.attend(q.double().cpu().numpy(), codes(c.k), c.k_scale.double().cpu().numpy(), codes(c.v),
+                                c.v_scale.double().cpu().numpy(), [0, 1, 2], lens, table)
+    other, streams = c.clone(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[h.attend(*args, stream=s) for h, s in zip((c, other), streams)] for _ in range(40)]
+    torch.cuda.synchronize()
+    for pair in outs:
+        for o in pair:
+            assert torch.equal(o, outs[0][0])
+    close(outs[0][0], want, bound, torch.float16)
+    assert c.status() == eva_vq.EVA_OK and other.status() == eva_vq.EVA_OK
+    other.close()
+    c.close()
+
+
 @pytest.mark.parametrize("B", [1, 5])
 def test_attention_half_of_a_block(B):
     """q, k and v layers in one launch, positions and cache, attention, the o layer: three steps on a prompt's cache,

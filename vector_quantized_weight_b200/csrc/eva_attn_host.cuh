@@ -482,6 +482,7 @@ eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t
     if (T == 0) return EVA_OK;
     const eva_kv_desc &d = h->desc;
     if (!row_ok(q, ldq, (int64_t)d.q_heads * d.head_dim, 2) || !out || !aligned16(out)) return EVA_ERR_INVALID_ARG;
+    if ((int64_t)T * (d.q_heads / d.kv_heads) > (1 << 30)) return EVA_ERR_UNSUPPORTED;      // rows of a key head are 32-bit
     DeviceGuard guard(h->device);
     if (!guard.ok) return EVA_ERR_CUDA;
     AttendParams p = {};

@@ -586,8 +586,10 @@ class HeadRope(_OnDevice):
         Tk, ldk = _rows("k", k, Hk, D, self.in_dtype, dev)
         if T != Tk:
             raise ValueError(f"q has {T} rows, k has {Tk}")
-        if self.rotary_dim or positions is not None:
+        if positions is not None:
             _indices("positions", positions, (T,), dev)
+        elif self.rotary_dim:
+            raise ValueError("positions are needed")
         if q_out is None:
             q_out, ldqo = self._empty((T, Hq, D), self.out_dtype, stream), Hq * D
         else:
