@@ -9,32 +9,39 @@
 // What bounds it: a decode step reads each cached byte once for a handful of
 // multiplications, so bytes; everything else has to fit beside the stream.
 //  - Codes become f16 exactly (int8: a byte under exponent 2^10, minus 1152;
-//    e4m3: the conversion instruction) and go
-//    to the tensor cores as the A operand: 16 tokens x 16 dimensions of keys,
-//    16 dimensions x 16 tokens of values.  Rows are the MMA's N (8 at a time),
-//    so a decode step of one to eight queries a key head wastes nothing, and
-//    more rows reuse the converted codes.  Warp-level MMAs: at eight rows the
-//    product is 2 % of the tensor rate at full stream speed; the conversion
-//    into registers is the work, and tcgen05 would take it through tensor
-//    memory first.
+//    e4m3: the conversion instruction -- shifting sign and magnitude into place
+//    kept the integer pipe 72 % busy and took half as long again on heads of
+//    256) and go to the tensor cores as the A operand: 16 tokens x 16
+//    dimensions of keys, 16 dimensions x 16 tokens of values.  Rows are the MMA's
+//    N, 8 at a time, so a decode step of one to eight queries a key head wastes
+//    nothing, and more rows reuse the converted codes.  Warp-level MMAs: at
+//    eight rows the tensor pipe is 11 % busy at full stream speed and the
+//    conversion into registers is the work.  With many rows (64 tokens of a
+//    prompt with eight queries a key head: 512) the products bound it, and
+//    these MMAs reach 172 TFLOP/s there, a tenth of what tcgen05 would.
 //  - Scales never touch the codes: sk multiplies the finished score, sv enters
-//    the exponent.  With w_j = e^(z_j - M) sv and M the running maximum of
-//    z_j + ln sv, the weights stay in (0, 1] whatever the pages' scales are;
-//    the sum of the softmax gets w_j / sv.  w_j is rounded to f16 (one
-//    2^-12 error a weight, averaged over the keys); all sums and statistics are
-//    fp32.
+//    the exponent.  With w_j = e^(z_j - M) sv and M a reference near the maximum
+//    of z_j + ln sv, the weights stay in (0, 256] whatever the pages' scales
+//    are; the sum of the softmax gets w_j / sv.  w_j is rounded to f16 for the
+//    value product (at most 2^-11 of it: the products run at the f16 rate and
+//    the error averages over the keys); all sums and statistics are fp32.
 //  - One warp of a CTA walks the work, looks pages and scales up, 32 steps at a
 //    time, one a lane, and copies each step's codes (TMA, swizzled: both
 //    ldmatrix patterns are free of bank conflicts) into a ring in shared
 //    memory; the others take turns at the steps.  (Copies issued by the warp
-//    that needs them, into buffers of its own, measured 10 us slower on 268 MB
-//    at 64 sequences: the issue then sits between a step's products.)  A page
-//    id outside the cache is never used as an address: its tokens count as
+//    that needs them, into buffers of its own, took 72 us for 268 MB of 64
+//    sequences against 64: the issue then sits between a step's products.)  A
+//    page id outside the cache is never used as an address: its tokens count as
 //    masked and the status word is set.
 //  - Work is cut on the device, because only the device knows the lengths
 //    (AtWalk).  An item (sequence, row tile, key head) that several CTAs share
 //    is joined by the last of them to finish, in the order of the parts, so
 //    results do not depend on timing.
+//
+// Measured (device time): 268 MB of cache as 64 sequences 58 us (4.7 TB/s), as
+// one 54 us (5.0 TB/s, of which 39 us stream at the memory's rate and the rest
+// is the start's three dependent lookups, the joins and the slowest CTAs); 517
+// tokens of 32 heads 10.1 us, all of it latency.
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -217,7 +224,8 @@ struct AtWalk {
     int off;                           // of the item that lies before this CTA's stretch; few items: which part of
     int k;                             // how many
 
-    static __device__ __forceinline__ int cuts(int n, int S) { return (n + S - 1) / S; }
+    // (an item half as long again as the least part stays whole: 17 steps in one part or two, 10.1 or 10.6 us)
+    static __device__ __forceinline__ int cuts(int n, int S, int least) { return 2 * n <= 3 * least ? 1 : (n + S - 1) / S; }
 
     __device__ __forceinline__ void init(const AttendParams &p, int rows, bool &bad) {
         const int lane = threadIdx.x & 31;
@@ -270,7 +278,7 @@ struct AtWalk {
             long long w = 0;
             for (int t = 0, n = at_tiles(s, rows, p.G); t < n; ++t) {
                 const int m = at_tile<TS>(s, t, rows, p.G, p.window).n;
-                w += few ? cuts(m, S) : m + kAtItemCost;
+                w += few ? cuts(m, S, p.min_steps) : m + kAtItemCost;
             }
             w *= p.H;
             long long sum = w;
@@ -296,7 +304,7 @@ struct AtWalk {
         int w = 1;
         for (rt = 0;; ++rt) {
             tile = at_tile<TS>(seq, rt, rows, p.G, p.window);
-            w = few ? cuts(tile.n, S) : tile.n + kAtItemCost;
+            w = few ? cuts(tile.n, S, p.min_steps) : tile.n + kAtItemCost;
             if (in < (long long)w * p.H || rt + 1 >= nrt) break;
             in -= (long long)w * p.H;
         }

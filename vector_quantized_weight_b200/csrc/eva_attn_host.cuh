@@ -28,7 +28,7 @@ struct eva_kv {
     float2 *part_ml = nullptr;
     int max_grid = 0;
     int64_t workspace_bytes = 0;
-    // attention instances: items of 8, 16 and 32 rows
+    // attention instances: items of 8, 16 and 24 or 32 rows
     struct Plan { const void *fn = nullptr; int rows = 0, stages = 0, grid = 0, threads = 0; size_t smem = 0; } plan[3];
     int last_plan = 0;
     int inject_wait_rounds = 0;        // failure-detection test hook, as for the linear
@@ -180,12 +180,16 @@ cudaError_t plan_attend(eva_kv *h, int i, int optin) {
     p.grid = per_sm * h->sm_count;
     return cudaSuccess;
 }
+// Warps and CTAs an SM, all measured (us, 517 tokens of 32 heads / 268 MB of 64 sequences / of one): for up to eight
+// rows two CTAs of 5 working warps 10.7 / 57.8 / 54.3, three of 4 11.7 / 55.5 / 54.0, two of 4 11.0 / 58.4 / 54.5,
+// four of 3 12.6 / 56.7 / 57.5, two of 7 11.5 / 61.9 / 55.9; heads of 256 two of 4 50.0 against two of 5 52.4.  More rows
+// take registers: one CTA of 7, and 24 rows an item at heads of 128 (32 would spill; at 64 they fit).
 template <int D, bool E4M3>
 cudaError_t plan_attends(eva_kv *h, int optin) {
     if constexpr (D <= 128) {
         cudaError_t e = plan_attend<D, 1, 5, 2, E4M3>(h, 0, optin);
         if (e == cudaSuccess) e = plan_attend<D, 2, 7, 1, E4M3>(h, 1, optin);
-        if (e == cudaSuccess) e = plan_attend<D, D < 128 ? 4 : 3, 7, 1, E4M3>(h, 2, optin);   // by registers again
+        if (e == cudaSuccess) e = plan_attend<D, D < 128 ? 4 : 3, 7, 1, E4M3>(h, 2, optin);
         return e;
     } else {                             // 16 rows a warp would not fit in its registers
         return plan_attend<D, 1, 4, 2, E4M3>(h, 0, optin);

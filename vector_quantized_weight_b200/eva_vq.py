@@ -464,11 +464,14 @@ def run_group(layers, xs, outs=None, stream=None, independent=False):
 # ------------------------------- between a block's q, k, v layers and its o layer
 
 _DTYPES = {}      # torch dtype or its name -> (torch dtype, eva_dtype_t); filled on first use
+_INT32 = None
 
 
 def _dtype(t):
+    global _INT32
     if not _DTYPES:
         import torch
+        _INT32 = torch.int32
         for d, code in ((torch.float16, EVA_F16), (torch.float32, EVA_F32)):
             _DTYPES[d] = _DTYPES[str(d).removeprefix("torch.")] = (d, code)
     if t not in _DTYPES:
@@ -493,38 +496,37 @@ def _rows(name, x, heads, head_dim, dtype, device):
 
 
 def _indices(name, x, shape, device):
-    if x.dtype != _INT32() or x.device != device or x.shape != shape or not x.is_contiguous():
+    if x.dtype != _INT32 or x.device != device or x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on {device}, "
                          f"not {x.dtype} {tuple(x.shape)} on {x.device}")
 
 
-def _INT32():
-    import torch
-    return torch.int32
-
-
 class _OnDevice:
-    """A handle on one device: its stream, and outputs that belong to the stream of the call."""
+    """A handle on one device: its stream, and outputs that belong to the stream of the call.  A decode step's calls
+    are a few microseconds of device time, so what a call needs of torch is looked up once."""
+
+    def _prepare(self):
+        import torch
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._empty_like, self._half, self._single = torch.empty_like, torch.float16, torch.float32
+        self._like = {d: torch.empty(0, dtype=d, device=self.device) for d in (torch.float16, torch.float32)}
 
     def _stream(self, stream):
-        import torch
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.device.index)
+            return self._raw_stream(self.device.index)
         if stream.device != self.device:
             raise ValueError(f"the stream is on {stream.device}, the handle on {self.device}")
         return stream.cuda_stream
 
-    def _empty(self, shape, dtype, stream):
-        """An output that belongs to the call's stream."""
-        import torch
+    def _empty(self, shape, dtype, stream, x=None):
+        """An output of the call's stream; x: an input that may have its shape and type (copying those is cheapest)."""
         if stream is None:
-            return self._like[dtype].new_empty(shape)       # cheaper than torch.empty with a type and a device
+            if x is not None and x.dtype == dtype and x.shape == shape and x.is_contiguous():
+                return self._empty_like(x)
+            return self._like[dtype].new_empty(shape)
+        import torch
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def _prototypes(self):
-        import torch
-        self._like = {d: torch.empty(0, dtype=d, device=self.device) for d in (torch.float16, torch.float32)}
 
     def __del__(self):
         try:
@@ -573,10 +575,10 @@ class HeadRope(_OnDevice):
                                   float(theta), float(how.get("factor", 1.0)), float(how.get("original", 0.0)),
                                   float(how.get("low", 1.0)), float(how.get("high", 4.0 if kind == "bands" else 32.0)),
                                   float(how.get("magnitude", 0.0)))
+        self._prepare()
         with torch.cuda.device(self.device):
             self.handle = eva_rope_create(self.desc, _ptr(q_weight), _ptr(k_weight), self._stream(stream))
         self._run = load().eva_rope_run
-        self._prototypes()
 
     def __call__(self, q, k, positions, q_out=None, k_out=None, stream=None):
         """(q_out, k_out) of q [T][q_heads][head_dim], k [T][kv_heads][head_dim] (rows may lie apart, as columns of
@@ -591,13 +593,13 @@ class HeadRope(_OnDevice):
         elif self.rotary_dim:
             raise ValueError("positions are needed")
         if q_out is None:
-            q_out, ldqo = self._empty((T, Hq, D), self.out_dtype, stream), Hq * D
+            q_out, ldqo = self._empty((T, Hq, D), self.out_dtype, stream, q), Hq * D
         else:
             To, ldqo = _rows("q_out", q_out, Hq, D, self.out_dtype, dev)
             if To != T:
                 raise ValueError(f"q_out has {To} rows, q has {T}")
         if k_out is None:
-            k_out, ldko = self._empty((T, Hk, D), self.out_dtype, stream), Hk * D
+            k_out, ldko = self._empty((T, Hk, D), self.out_dtype, stream, k), Hk * D
         else:
             To, ldko = _rows("k_out", k_out, Hk, D, self.out_dtype, dev)
             if To != T:
@@ -656,10 +658,10 @@ class KVCache(_OnDevice):
         self.desc = eva_kv_desc(self.q_heads, self.kv_heads, self.head_dim, int(page_size), int(num_pages), self.max_seqs,
                                 self.max_pages, EVA_CACHE_INT8 if dtype == "int8" else EVA_CACHE_E4M3, code_out,
                                 int(window), float(softcap), float(scale or 0.0))
+        self._prepare()
         with torch.cuda.device(self.device):
             self.handle = eva_kv_create(self.desc, *map(_ptr, made), self._stream(stream))
         lib = load()
-        self._prototypes()
         self._append, self._attend, self._read = lib.eva_kv_append, lib.eva_kv_attend, lib.eva_kv_read
 
     def clone(self, **changes):
@@ -696,15 +698,14 @@ class KVCache(_OnDevice):
     def attend(self, q, starts, lens, page_table, out=None, lse=None, stream=None):
         """Causal attention of q fp16 [T][q_heads][head_dim] over the cache -> [T][q_heads][head_dim].  Rows
         behind starts[B] are not written: give `out` where they matter.  lse: optional float32 [T][q_heads]."""
-        import torch
         B = self._sequences(starts, lens, page_table)
         Hq, D, dev = self.q_heads, self.head_dim, self.device
-        T, ldq = _rows("q", q, Hq, D, torch.float16, dev)
+        T, ldq = _rows("q", q, Hq, D, self._half, dev)
         if out is None:
-            out = self._empty((T, Hq, D), self.out_dtype, stream)
+            out = self._empty((T, Hq, D), self.out_dtype, stream, q)
         elif _rows("out", out, Hq, D, self.out_dtype, dev) != (T, Hq * D):
             raise ValueError(f"out must be a contiguous [{T}][{Hq}][{D}] tensor")
-        if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != (T, Hq) or
+        if lse is not None and (lse.dtype != self._single or lse.device != dev or lse.shape != (T, Hq) or
                                 not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous float32 tensor ({T}, {Hq}) on {dev}")
         rc = self._attend(self.handle, q.data_ptr(), ldq, starts.data_ptr(), lens.data_ptr(), page_table.data_ptr(), B, T,
