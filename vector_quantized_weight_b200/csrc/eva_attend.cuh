@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
     };
 
     float o[NT][kChunks][4], m[NT][2], l[NT][2];
-    int last[NT][2], pmin = 0, pmax = 0;       // the last key each row of this lane sees, and of the item's rows
+    int pmin = 0, pmax = 0;            // the last key that the item's first and its last row see
     int ps = 0, ct = warp;             // the piece's place; this warp's next step of the CTA
     int own = warp;                    // and its stage, and that stage's parity
     uint32_t pparity = 0, own_parity = 0;
@@ -665,7 +665,6 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    last[nt][e] = pos0 + (r0 + min(nrows - 1, nt * 8 + 2 * c + e)) / p.G;
                     m[nt][e] = -INFINITY;
                     l[nt][e] = 0.f;
                 }
@@ -747,12 +746,14 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                             z[nt][mt][e] = z[nt][mt][e] * (sc.sk[mt] * zscale) + sc.lsv[mt];
                         }
                     }
-                if (edge) {
+                if (edge) {                    // (few steps: worked out here rather than kept in registers)
+                    const int r0 = bt.rt * kRows, rl = min(kRows, bt.rows * p.G - r0) - 1, pos0 = bt.len - bt.rows;
+                    const int last[2] = {pos0 + (r0 + min(rl, nt * 8 + 2 * c)) / p.G, pos0 + (r0 + min(rl, nt * 8 + 2 * c + 1)) / p.G};
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = tok0 + mt * 16 + g + (e >> 1) * 8, pos = last[nt][e & 1];
+                            const int j = tok0 + mt * 16 + g + (e >> 1) * 8, pos = last[e & 1];
                             if (j > pos || (p.window > 0 && j <= pos - p.window) || sc.sk[mt] < 0.f)
                                 z[nt][mt][e] = -INFINITY;
                         }

@@ -182,14 +182,14 @@ cudaError_t plan_attend(eva_kv *h, int i, int optin) {
 }
 // Warps and CTAs an SM, all measured (us, 517 tokens of 32 heads / 268 MB of 64 sequences / of one): for up to eight
 // rows two CTAs of 5 working warps 10.7 / 57.8 / 54.3, three of 4 11.7 / 55.5 / 54.0, two of 4 11.0 / 58.4 / 54.5,
-// four of 3 12.6 / 56.7 / 57.5, two of 7 11.5 / 61.9 / 55.9; heads of 256 two of 4 50.0 against two of 5 52.4.  More rows
-// take registers: one CTA of 7, and 24 rows an item at heads of 128 (32 would spill; at 64 they fit).
+// four of 3 12.6 / 56.7 / 57.5, two of 7 11.5 / 61.9 / 55.9; heads of 256 two of 4 50.0 against two of 5 52.4.  Many
+// rows take registers: one CTA of 7, with 32 rows an item where they fit (int8 at heads of 128 would spill: 24).
 template <int D, bool E4M3>
 cudaError_t plan_attends(eva_kv *h, int optin) {
     if constexpr (D <= 128) {
         cudaError_t e = plan_attend<D, 1, 5, 2, E4M3>(h, 0, optin);
-        if (e == cudaSuccess) e = plan_attend<D, 2, 7, 1, E4M3>(h, 1, optin);
-        if (e == cudaSuccess) e = plan_attend<D, D < 128 ? 4 : 3, 7, 1, E4M3>(h, 2, optin);
+        if (e == cudaSuccess) e = plan_attend<D, 2, 5, 2, E4M3>(h, 1, optin);
+        if (e == cudaSuccess) e = plan_attend<D, D < 128 || E4M3 ? 4 : 3, 7, 1, E4M3>(h, 2, optin);
         return e;
     } else {                             // 16 rows a warp would not fit in its registers
         return plan_attend<D, 1, 4, 2, E4M3>(h, 0, optin);
@@ -512,9 +512,11 @@ eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t
     h->inject_wait_rounds = 0;
     p.scale = d.scale > 0 ? d.scale : 1.0f / std::sqrt((float)d.head_dim);
     p.cap = d.softcap;
-    // rows of a sequence and key head, on average (the real counts are on the device)
+    // Rows of a sequence and key head, on average (the real counts are on the device).  Up to 64, items of 16 rows with
+    // more warps an SM (us, items of 16 / of 24 or 32: 32 rows 26 / 33, 40 rows 18 / 23, 64 rows 22.2 / 22.9, 128 rows
+    // 40 / 37, 512 rows 108 / 100).
     const int64_t rows = (T + B - 1) / B * (int64_t)p.G;
-    int i = rows <= 8 ? 0 : rows <= 16 ? 1 : 2;
+    int i = rows <= 8 ? 0 : rows <= 64 ? 1 : 2;
     while (!h->plan[i].fn) --i;
     h->last_plan = i;
     const eva_kv::Plan &pl = h->plan[i];
