@@ -339,22 +339,30 @@ eva_status_t eva_rope_run(eva_rope_t h, const void *q, int64_t ldq, const void *
     p.interleaved = d.layout == EVA_ROPE_INTERLEAVED;
     p.norm = d.norm;
     p.eps = d.eps; p.offset = d.weight_offset; p.magnitude = h->magnitude;
-    // 16-byte accesses where every row allows them
+    // 16-byte accesses where every row allows them (and 8 rows' offsets fit 32 bits)
     const int bi = dtype_bytes(d.in_dtype), bo = dtype_bytes(d.out_dtype);
-    auto wide = [](const void *a, int64_t ld, int bytes) { return aligned16(a) && ld * bytes % 16 == 0; };
+    auto wide = [](const void *a, int64_t ld, int bytes) { return aligned16(a) && ld * bytes % 16 == 0 && ld <= 1 << 27; };
     int lanes = 0;
     if (d.head_dim % 16 == 0 && d.rotary_dim % 16 == 0 && d.head_dim <= 512 &&
         (!d.q_heads || (wide(q, ldq, bi) && wide(q_out, ldqo, bo))) &&
         (!d.kv_heads || (wide(k, ldk, bi) && wide(k_out, ldko, bo))))
         for (lanes = 4; lanes * 16 < d.head_dim;) lanes *= 2;
-    // Few tokens: one a CTA, and as many heads as its lanes hold at once, until that fills the GPU.  Then whole tokens,
-    // and as many (1 to 8) as leave three CTAs an SM: a CTA computes its tokens' sines once.
+    // Few tokens: one a CTA, and as many heads as its lanes hold at once, until that fills the GPU.  Then whole tokens, 1
+    // to 8 a CTA: a CTA's cost is its turns and about two more for the sines, its waves (three CTAs an SM) end half
+    // a wave late.  (8192 tokens of 72 heads: 4 a CTA 63 us, 8 67; 1777 of 40 heads: 4 10.9, 1 12.0.)
     const int groups = lanes ? kRopeThreads / lanes : kRopeThreads / 32;
     p.tb = 1;
     p.hs = std::min(p.H, groups);
     if ((int64_t)T * ((p.H + p.hs - 1) / p.hs) > (int64_t)h->sm_count * 4) {
         p.hs = p.H;
-        while (p.tb < 8 && T >= (int64_t)h->sm_count * 6 * p.tb) p.tb *= 2;
+        double least = 0;
+        for (int tb = 1; tb <= 8; tb *= 2) {
+            const double cost = ((double)((T + tb - 1) / tb) / (3 * h->sm_count) + 0.5) * ((tb * (int64_t)p.H + groups - 1) / groups + 2);
+            if (tb == 1 || cost < least * 0.99) {
+                least = cost;
+                p.tb = tb;
+            }
+        }
     }
     const dim3 grid((unsigned)((T + p.tb - 1) / p.tb), (unsigned)((p.H + p.hs - 1) / p.hs));
     const size_t smem = (size_t)p.tb * (d.rotary_dim / 2) * 2 * sizeof(float) + (lanes && d.norm ? 2 * d.head_dim * sizeof(float) : 0);

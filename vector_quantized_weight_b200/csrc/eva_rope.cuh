@@ -150,10 +150,11 @@ struct RopeRaw {
 // W lanes a head (a power of two >= D/16).  Needs D and R multiples of 16, and
 // every pointer and stride a multiple of 16 bytes.  A lane keeps the loads of its
 // next turns in flight (with one turn's, a prompt of 8192 tokens and 72 heads of
-// 128 took 86 us: 24 KB an SM are too few for the memory's latency).
+// 128 took 86 us: 24 KB an SM are too few for the memory's latency; now 63 us, 4.8
+// TB/s, bound by instruction issue beside the memory).
 template <typename TI, typename TO, int W>
 __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p) {
-    constexpr int kAhead = sizeof(TI) == 2 ? 3 : 1;
+    constexpr int kAhead = sizeof(TI) == 2 ? 2 : 1;
     float *ws = reinterpret_cast<float *>(eva_smem);       // weight + offset (or 1) of queries and of keys
     float *cos = ws + (p.norm ? 2 * p.D : 0), *sin = cos + p.tb * (p.R >> 1);
     const int unit = threadIdx.x % W, group = threadIdx.x / W, groups = kRopeThreads / W;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p)
     const bool live = unit * 16 < p.D, turned = unit * 16 < p.R;
     // the two chunks of this lane
     const bool split = turned && !p.interleaved;
-    const int oa = split ? unit * 8 : unit * 16, ob = split ? half + unit * 8 : oa + 8;
+    const int oa = split ? unit * 8 : unit * 16, ob = split ? half : 8;    // ob: from the first
     if (p.norm)
         for (int i = threadIdx.x; i < 2 * p.D; i += kRopeThreads) {
             const __half *w = i < p.D ? p.qw : p.kw;
@@ -187,22 +188,27 @@ __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p)
         }
     };
     At in = {group / nh, group % nh}, out = in;
+    // this CTA's first token, head h0 (the keys' pointers count the query heads in), this lane's first chunk; within
+    // the CTA offsets are 32-bit
+    const int nq = p.Hq - h0, ldq = (int)p.ldq, ldk = (int)p.ldk, ldqo = (int)p.ldqo, ldko = (int)p.ldko;
+    const TI *q0 = static_cast<const TI *>(p.q) + t0 * p.ldq + (h0 * p.D + oa);
+    const TI *k0 = static_cast<const TI *>(p.k) + t0 * p.ldk + (oa - nq * p.D);
+    TO *qo0 = static_cast<TO *>(p.qo) + t0 * p.ldqo + (h0 * p.D + oa);
+    TO *ko0 = static_cast<TO *>(p.ko) + t0 * p.ldko + (oa - nq * p.D);
     auto load = [&](RopeRaw<TI> &r) {
-        const int t = t0 + in.t, h = h0 + in.h;
-        const bool on = in.t < nt && live;
+        const bool on = in.t < nt && live, isq = in.h < nq;
+        const TI *src = (isq ? q0 : k0) + (in.t * (isq ? ldq : ldk) + in.h * p.D);
         step(in);
-        if (!on) return;
-        const TI *src = h < p.Hq ? static_cast<const TI *>(p.q) + t * p.ldq + (long long)h * p.D
-                                 : static_cast<const TI *>(p.k) + t * p.ldk + (long long)(h - p.Hq) * p.D;
-        r.load(src + oa, src + ob);
+        if (on) r.load(src, src + ob);
     };
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) load(raw[j]);      // in flight while the angles are computed
     rope_angles(p, t0, nt, cos, sin);
     __syncthreads();
     auto turn = [&](const RopeRaw<TI> &r) {
-        const int t = out.t, h = h0 + out.h;
-        const bool on = t < nt && live;
+        const int t = out.t;
+        const bool on = t < nt && live, isq = out.h < nq;
+        TO *dst = (isq ? qo0 : ko0) + (t * (isq ? ldqo : ldko) + out.h * p.D);
         step(out);
         F2 a[4], b[4];
         r.get(a, b);
@@ -218,10 +224,10 @@ __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p)
             for (int o = W / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, W);
             const float s = rsqrtf(ss * inv_d + p.eps);
             if (on) {
-                const float *w = ws + (h < p.Hq ? 0 : p.D);
+                const float *w = ws + (isq ? oa : p.D + oa);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float4 wa = reinterpret_cast<const float4 *>(w + oa)[j], wb = reinterpret_cast<const float4 *>(w + ob)[j];
+                    const float4 wa = reinterpret_cast<const float4 *>(w)[j], wb = reinterpret_cast<const float4 *>(w + ob)[j];
                     a[2 * j] = f2_mul(f2_mul(a[2 * j], {s, s}), {wa.x, wa.y});
                     a[2 * j + 1] = f2_mul(f2_mul(a[2 * j + 1], {s, s}), {wa.z, wa.w});
                     b[2 * j] = f2_mul(f2_mul(b[2 * j], {s, s}), {wb.x, wb.y});
@@ -254,9 +260,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p)
                 }
             }
         }
-        TO *dst = h < p.Hq ? static_cast<TO *>(p.qo) + (t0 + t) * p.ldqo + (long long)h * p.D
-                           : static_cast<TO *>(p.ko) + (t0 + t) * p.ldko + (long long)(h - p.Hq) * p.D;
-        rope_store8(dst + oa, reinterpret_cast<const float(&)[8]>(a));
+        rope_store8(dst, reinterpret_cast<const float(&)[8]>(a));
         rope_store8(dst + ob, reinterpret_cast<const float(&)[8]>(b));
     };
     // every group takes the same number of turns, so the shuffles see whole warps
