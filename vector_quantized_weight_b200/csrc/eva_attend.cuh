@@ -18,7 +18,7 @@
 //    eight rows the tensor pipe is 11 % busy at full stream speed and the
 //    conversion into registers is the work.  With many rows (64 tokens of a
 //    prompt with eight queries a key head: 512) the products bound it, and
-//    these MMAs reach 172 TFLOP/s there, a tenth of what tcgen05 would.
+//    these MMAs reach 170 TFLOP/s there, a tenth of the tensor peak.
 //  - Scales never touch the codes: sk multiplies the finished score, sv enters
 //    the exponent.  With w_j = e^(z_j - M) sv and M a reference near the maximum
 //    of z_j + ln sv, the weights stay in (0, 256] whatever the pages' scales
