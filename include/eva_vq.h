@@ -446,7 +446,7 @@ EVA_API eva_status_t eva_rope_create(eva_rope_t *out, const eva_rope_desc *desc,
  * input types' arithmetic is fp32, rounded once.  q_out may be q (k_out k) when
  * the types and strides are equal; otherwise outputs must not overlap inputs.
  * Any alignment of the element type works; 16-byte aligned rows with head_dim
- * and rotary_dim multiples of 16 are faster.
+ * (and in the half layout rotary_dim) a multiple of 16 are faster.
  */
 EVA_API eva_status_t eva_rope_run(eva_rope_t h, const void *q, int64_t ldq, const void *k, int64_t ldk,
                                   const int32_t *positions, int32_t T, void *q_out, int64_t ldqo, void *k_out,

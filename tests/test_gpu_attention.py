@@ -48,6 +48,8 @@ ROPE = [
     (4, 2, 1, 35, 34, "interleaved", None, True, "float32", "float32"),
     (5, 1, 1, 512, 512, "half", None, False, "float16", "float16"),
     (3, 1, 1, 1000, 998, "half", None, True, "float16", "float16"),
+    (700, 3, 2, 64, 24, "interleaved", None, True, "float16", "float16"),    # the last 16 turned dimensions half
+    (40, 2, 1, 256, 2, "interleaved", {"type": "yarn", "factor": 4.0, "original": 100}, False, "float32", "float16"),
     (6, 4, 4, 128, 0, "half", None, True, "float16", "float16"),             # the norm alone
     (6, 0, 4, 128, 128, "half", None, False, "float16", "float16"),          # keys alone
     (2500, 2, 1, 64, 64, "half", None, False, "float16", "float16"),         # four tokens a CTA

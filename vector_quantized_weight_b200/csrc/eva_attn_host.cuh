@@ -343,7 +343,7 @@ eva_status_t eva_rope_run(eva_rope_t h, const void *q, int64_t ldq, const void *
     const int bi = dtype_bytes(d.in_dtype), bo = dtype_bytes(d.out_dtype);
     auto wide = [](const void *a, int64_t ld, int bytes) { return aligned16(a) && ld * bytes % 16 == 0 && ld <= 1 << 27; };
     int lanes = 0;
-    if (d.head_dim % 16 == 0 && d.rotary_dim % 16 == 0 && d.head_dim <= 512 &&
+    if (d.head_dim % 16 == 0 && (d.rotary_dim % 16 == 0 || p.interleaved) && d.head_dim <= 512 &&
         (!d.q_heads || (wide(q, ldq, bi) && wide(q_out, ldqo, bo))) &&
         (!d.kv_heads || (wide(k, ldk, bi) && wide(k_out, ldko, bo))))
         for (lanes = 4; lanes * 16 < d.head_dim;) lanes *= 2;
@@ -365,7 +365,7 @@ eva_status_t eva_rope_run(eva_rope_t h, const void *q, int64_t ldq, const void *
         }
     }
     const dim3 grid((unsigned)((T + p.tb - 1) / p.tb), (unsigned)((p.H + p.hs - 1) / p.hs));
-    const size_t smem = (size_t)p.tb * (d.rotary_dim / 2) * 2 * sizeof(float) + (lanes && d.norm ? 2 * d.head_dim * sizeof(float) : 0);
+    const size_t smem = (size_t)p.tb * rope_row(d.rotary_dim) * 2 * sizeof(float) + (lanes && d.norm ? 2 * d.head_dim * sizeof(float) : 0);
     return cuda_status(launch_pdl(rope_fn(d.in_dtype, d.out_dtype, lanes), grid, dim3(kRopeThreads), smem,
                                   reinterpret_cast<cudaStream_t>(stream), 0, p));
 }

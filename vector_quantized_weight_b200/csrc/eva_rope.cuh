@@ -44,16 +44,23 @@ struct RopeParams {
     float eps, offset, magnitude;
 };
 
-// cos and sin of the tokens t0 .. t0 + nt - 1, [token][pair] each, by the whole CTA.
+// Pairs of a token's row in the tables: a multiple of 8, the ones behind the last turned by nothing (1, 0).
+__host__ __device__ __forceinline__ int rope_row(int R) { return (R / 2 + 7) & ~7; }
+
+// cos and sin of the tokens t0 .. t0 + nt - 1, [token][rope_row] each, by the whole CTA.
 __device__ __forceinline__ void rope_angles(const RopeParams &p, int t0, int nt, float *cos, float *sin) {
-    const int half = p.R >> 1;
-    for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-        const int t = i / half, j = i - t * half;
-        const unsigned long long a = (unsigned long long)(long long)p.pos[t0 + t] * p.turns[j];
-        float s, c;
-        sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns in [-1, 1)
-        cos[i] = c * p.magnitude;
-        sin[i] = s * p.magnitude;
+    const int half = p.R >> 1, row = rope_row(p.R);
+    for (int i = threadIdx.x; i < nt * row; i += blockDim.x) {
+        const int t = i / row, j = i - t * row;
+        float s = 0.f, c = 1.f;
+        if (j < half) {
+            const unsigned long long a = (unsigned long long)(long long)p.pos[t0 + t] * p.turns[j];
+            sincospif((float)(int32_t)(a >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns in [-1, 1)
+            c *= p.magnitude;
+            s *= p.magnitude;
+        }
+        cos[i] = c;
+        sin[i] = s;
     }
 }
 
@@ -147,8 +154,8 @@ struct RopeRaw {
     }
 };
 
-// W lanes a head (a power of two >= D/16).  Needs D and R multiples of 16, and
-// every pointer and stride a multiple of 16 bytes.  A lane keeps the loads of its
+// W lanes a head (a power of two >= D/16).  Needs D a multiple of 16, R too in the
+// half layout, and every pointer and stride a multiple of 16 bytes.  A lane keeps the loads of its
 // next turns in flight (with one turn's, a prompt of 8192 tokens and 72 heads of
 // 128 took 86 us: 24 KB an SM are too few for the memory's latency; now 63 us, 4.8
 // TB/s, bound by instruction issue beside the memory).
@@ -156,7 +163,7 @@ template <typename TI, typename TO, int W>
 __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p) {
     constexpr int kAhead = sizeof(TI) == 2 ? 2 : 1;
     float *ws = reinterpret_cast<float *>(eva_smem);       // weight + offset (or 1) of queries and of keys
-    float *cos = ws + (p.norm ? 2 * p.D : 0), *sin = cos + p.tb * (p.R >> 1);
+    float *cos = ws + (p.norm ? 2 * p.D : 0), *sin = cos + p.tb * rope_row(p.R);
     const int unit = threadIdx.x % W, group = threadIdx.x / W, groups = kRopeThreads / W;
     const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0), half = p.R >> 1;
     const bool live = unit * 16 < p.D, turned = unit * 16 < p.R;
@@ -237,8 +244,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p)
         }
         if (!on) return;
         if (turned) {
-            const float4 *cr = reinterpret_cast<const float4 *>(cos + t * half + unit * 8);
-            const float4 *sr = reinterpret_cast<const float4 *>(sin + t * half + unit * 8);
+            const int at = t * rope_row(p.R) + unit * 8;
+            const float4 *cr = reinterpret_cast<const float4 *>(cos + at), *sr = reinterpret_cast<const float4 *>(sin + at);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float4 c = cr[j], n = sr[j];
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p)
 
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) eva_rope_any_kernel(RopeParams p) {
-    float *cos = reinterpret_cast<float *>(eva_smem), *sin = cos + p.tb * (p.R >> 1);
+    float *cos = reinterpret_cast<float *>(eva_smem), *sin = cos + p.tb * rope_row(p.R);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t0 = blockIdx.x * p.tb, nt = min(p.tb, p.T - t0), half = p.R >> 1;
     pdl_wait();
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(kRopeThreads) eva_rope_any_kernel(RopeParams p
         };
         for (int j = lane; j < half; j += 32) {
             const int ja = p.interleaved ? 2 * j : j, jb = p.interleaved ? 2 * j + 1 : j + half;
-            const float2 c = make_float2(cos[t * half + j], sin[t * half + j]);
+            const float2 c = make_float2(cos[t * rope_row(p.R) + j], sin[t * rope_row(p.R) + j]);
             const float xa = scaled(ja), xb = scaled(jb);
             dst[ja] = (TO)(xa * c.x - xb * c.y);
             dst[jb] = (TO)(xb * c.x + xa * c.y);
