@@ -44,7 +44,7 @@ struct RopeParams {
     float eps, offset, magnitude;
 };
 
-// Pairs of a token's row in the tables: a multiple of 8, the ones behind the last turned by nothing (1, 0).
+// Pairs of a token's row in the tables: a multiple of 8 (the ones behind the last are not used).
 __host__ __device__ __forceinline__ int rope_row(int R) { return (R / 2 + 7) & ~7; }
 
 // cos and sin of the tokens t0 .. t0 + nt - 1, [token][rope_row] each, by the whole CTA.
@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p)
                     const float cc[4] = {c.x, c.y, c.z, c.w}, nn[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        // (pairs behind the last turned one are copies: a product with 0 would carry an infinity over)
                         const F2 x = v[i];
-                        v[i] = f2_fma({x.y, x.x}, {-nn[i], nn[i]}, f2_mul(x, {cc[i], cc[i]}));
+                        if (unit * 8 + 4 * j + i < half) v[i] = f2_fma({x.y, x.x}, {-nn[i], nn[i]}, f2_mul(x, {cc[i], cc[i]}));
                     }
                 }
             }
