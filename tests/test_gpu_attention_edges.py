@@ -1,5 +1,6 @@
 """Rotary positions, the 8-bit cache and attention over it where numbers, rows or pages are unusual: infinities and
 NaN, dominating keys, large caps, released pages, very many parts, waits that run out, other streams."""
+import numpy as np
 import pytest
 import torch
 
@@ -42,3 +43,24 @@ def test_rope_keeps_infinities_and_nans_where_they_are(T, D, R, layout, tin, tou
     rest = [d for d in range(R) if d not in pair]
     assert not torch.isfinite(got[:, 1, pair]).any() and torch.equal(got[:, 1, rest], clean[:, 1, rest])
     rope.close()
+
+
+# ------------------------------------------------------------------ attention
+
+def test_attend_sums_of_pages_of_zero_values():
+    """2,200,000 keys whose values are all zero: zeros, and the logarithm of a sum that keeps within fp32."""
+    P, D, total = 256, 64, 2200000
+    pages = -(-total // P)
+    c = eva_vq.KVCache(1, 1, D, num_pages=pages, max_seqs=1, max_pages=pages, page_size=P, out_dtype="float32")
+    c.k.random_(-60, 61, generator=torch.Generator(device="cuda").manual_seed(3))
+    c.k[0, 0, 32:] = 0
+    c.k_scale.fill_(0.01)
+    q = cuda(0.5 * rng(3).standard_normal((1, 1, D)), torch.float16)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages)
+    lse = torch.empty((1, 1), device="cuda")
+    out = c.attend(q, i32([0, 1]), i32([total]), table, lse=lse)
+    assert c.status() == eva_vq.EVA_OK and torch.all(out == 0)
+    z = (c.k.view(-1, D)[:total].float() @ q[0, 0].float()).double() * float(np.float32(0.01)) * D ** -0.5
+    # of the 2^-24 of exponents near 100 that a logarithm, a score and the reference lose each, and some 100 fp32 sums
+    assert abs(float(torch.logsumexp(z, 0)) - float(lse)) <= 3e-5
+    c.close()

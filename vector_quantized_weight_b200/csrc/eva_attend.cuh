@@ -356,8 +356,8 @@ struct AtWalk {
 // --------------------------------------------------------------- the kernel
 
 // What the walking warp leaves beside a step's codes, for each 16 tokens: the
-// score's factor (negative: no token there), log2 of the value scale, and one
-// over it.
+// score's factor (negative: no token there), log2 of the value scale, and
+// kAtSumScale over it.
 struct alignas(16) AtScales {
     float sk[2], lsv[2], rsv[2];
     int tag, pad;                      // the step's number in its CTA
@@ -374,6 +374,9 @@ constexpr int kAtPieces = 2;           // handed over ahead, with their queries 
 constexpr int kAtTurn = 2;             // steps copied at a time (divides 8)
 constexpr int kAtSmemPerSm = 228 * 1024;
 constexpr int kAtSegment = 8;          // parts that are joined at a time
+// A page of zeros counts as one of a very small value scale, so that it leaves the reference to the others: weights over
+// that scale are as large as 2^108, and 2^20 of them would leave fp32.  The sums are kept 2^20 times smaller.
+constexpr float kAtLeastScale = 1e-30f, kAtSumScale = 9.5367431640625e-07f, kAtLog2SumScale = -20.f;
 
 template <int D, int NT, int WARPS, int CTAS>
 struct AtShape {
@@ -553,10 +556,10 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                     AtScales sc = {};
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        const float v = fmaxf(sv[i], 1e-30f);
+                        const float v = fmaxf(sv[i], kAtLeastScale);
                         sc.sk[i] = sk[i];
                         sc.lsv[i] = log2f(v);
-                        sc.rsv[i] = 1.f / v;
+                        sc.rsv[i] = kAtSumScale / v;
                     }
                     const int count = min(32, n - s0);
                     // kAtTurn lanes at a time wait for their stages and fill them: one step at a time took the warp
@@ -885,7 +888,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
             auto slot_of = [&](int cc) { return (size_t)(2 * cc + (cc == c0)); };    // a CTA begins at most one shared item
             auto emit = [&](int r, int x, const float4 &v, float mm, float ll) {
                 const int i = (e0 + r) / p.G, hq = eh * p.G + (e0 + r) - i * p.G;
-                const float f = ll > 0.f ? 1.f / ll : 0.f;
+                const float f = ll > 0.f ? kAtSumScale / ll : 0.f;
                 const long long at = ((long long)(erow + i) * p.Hq + hq) * D + x;
                 if (p.out_f32) {
                     *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
@@ -896,7 +899,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
                 }
                 if (p.lse && x == 0)
-                    p.lse[(long long)(erow + i) * p.Hq + hq] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                    p.lse[(long long)(erow + i) * p.Hq + hq] = ll > 0.f ? (mm + (log2f(ll) - kAtLog2SumScale)) * 0.6931471805599453f : -INFINITY;
             };
 #pragma unroll 1
             for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
