@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests.conftest import cuda_available
-from tests.test_gpu_attention import cuda, i32, rng
+from tests.test_gpu_attention import close, codes, cuda, i32, rng
 from vector_quantized_weight_b200 import eva_vq
 
 pytestmark = [pytest.mark.gpu,
@@ -46,6 +46,90 @@ def test_rope_keeps_infinities_and_nans_where_they_are(T, D, R, layout, tin, tou
 
 
 # ------------------------------------------------------------------ attention
+
+def packed(tokens, P):
+    """[tokens][H][D] -> pages [pages][H][P][D], zeros behind the last token."""
+    n, H, D = tokens.shape
+    pages = -(-n // P)
+    x = np.zeros((pages * P, H, D), tokens.dtype)
+    x[:n] = tokens
+    return x.reshape(pages, P, H, D).transpose(0, 2, 1, 3)
+
+
+def one_sequence(cache, P, Hq, k, v, sk, sv, **kw):
+    """A cache that holds one sequence: code numbers k, v [tokens][H][D], scales [pages][H]; pages in order."""
+    kind = torch.int8 if cache == "int8" else torch.float8_e4m3fn
+    ts = [cuda(packed(np.asarray(x, np.float32), P)).to(kind) for x in (k, v)]
+    assert all(np.array_equal(codes(t), packed(np.asarray(x, np.float64), P)) for t, x in zip(ts, (k, v)))
+    pages, H, _, D = ts[0].shape
+    c = eva_vq.KVCache(Hq, H, D, num_pages=pages, max_seqs=1, max_pages=pages, page_size=P, dtype=cache, k=ts[0], v=ts[1],
+                       k_scale=cuda(sk, torch.float32), v_scale=cuda(sv, torch.float32), **kw)
+    return c, torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages)
+
+
+def softmax_of(q, k, v, sk, sv, P, scale, softcap=0.0):
+    """Rows q [n][Hq][D] at the last n positions of one sequence: outputs, lse and the error bound of an output before it is
+    rounded, in 64 bits.
+
+    The bound.  A weight w_j = p_j sv_j is rounded to fp16, 11 bits or a step of 2^-25 with the largest of them at 2^11
+    or more: 2^-11 w_j + 2^-36 max w.  A score is off by dz: its fp32 sums and products (as in attn_reference, relative
+    to the sum of their sizes) and, capped, by 2^-18 of itself; it enters a weight and the sum, so twice.  The fp32
+    sums of a warp's and a part's products: 2e-6."""
+    n, Hq, D = q.shape
+    total, H, _ = k.shape
+    G, page = Hq // H, np.arange(total) // P
+    out, lse, bound = np.zeros((n, Hq, D)), np.zeros((n, Hq)), np.zeros((n, Hq, D))
+    for hq in range(Hq):
+        h = hq // G
+        fk, fv = k[:, h] * sk[page, h][:, None], np.abs(v[:, h])
+        for i in range(n):
+            end = total - n + i + 1
+            z = fk[:end] @ q[i, hq] * scale
+            dz = 32 * 2.0 ** -24 * (np.abs(fk[:end]) @ np.abs(q[i, hq])) * scale + 4e-7 * np.abs(z).max()
+            if softcap:
+                z = softcap * np.tanh(z / softcap)
+                dz = dz + 2.0 ** -18 * np.abs(z)
+            m = z.max()
+            p = np.exp(z - m)
+            l, w = p.sum(), p * sv[page[:end], h]
+            out[i, hq], lse[i, hq] = w @ v[:end, h] / l, m + np.log(l)
+            bound[i, hq] = (2.0 ** -11 + 2 * dz.max() + 2e-6) * (w @ fv[:end]) / l + 2.0 ** -36 * w.max() * fv[:end].sum(0) / l
+    return out, lse, bound
+
+
+@pytest.mark.parametrize("cache,P,Hq,D,total,n,gap,scale_of_first", [
+    ("int8", 64, 1, 128, 131072, 1, 14.0, 60.0), ("e4m3", 64, 8, 64, 131071, 1, 18.0, 1.0),
+    ("int8", 16, 2, 64, 4097, 1, 14.0, 100.0), ("int8", 64, 8, 128, 5000, 2, 7.0, 1000.0),
+    ("e4m3", 32, 4, 256, 20001, 1, 10.0, 1000.0), ("int8", 128, 8, 128, 9000, 12, 14.0, 60.0),
+    ("e4m3", 64, 8, 64, 9001, 9, 16.0, 10.0), ("int8", 64, 1, 256, 4097, 5, 9.0, 500.0),
+])
+def test_attend_keeps_the_tail_beside_a_dominating_key(cache, P, Hq, D, total, n, gap, scale_of_first):
+    """The first token takes nearly all the softmax (or its page has by far the largest value scale) and its own values are
+    zero, as a first token's often are: the output is the tail's, and right relative to itself."""
+    r = rng(int(total + gap))
+    pages = -(-total // P)
+    k, v = np.zeros((total, 1, D)), r.integers(16, 31, (total, 1, D)).astype(float)
+    if cache == "e4m3":
+        v = np.floor(v / 2) * 2                  # 16 .. 30 in steps of 2: e4m3 numbers
+    k[1:, 0, 0] = r.integers(-2, 3, total - 1)
+    k[0, 0, 1] = 96.0
+    v[0] = 0.0
+    sk, sv = np.full((pages, 1), 0.125), np.full((pages, 1), 0.03125)
+    sv[0] *= scale_of_first
+    scale = D ** -0.5
+    q = 0.01 * r.standard_normal((n, Hq, D))
+    q[..., 0], q[..., 1] = 1.0, gap / (96 * 0.125 * scale)
+    q = cuda(q, torch.float16)
+    c, table = one_sequence(cache, P, Hq, k, v, sk, sv, out_dtype="float32")
+    lse = torch.empty((n, Hq), device="cuda")
+    out = c.attend(q, i32([0, n]), i32([total]), table, lse=lse)
+    assert c.status() == eva_vq.EVA_OK
+    want, wlse, bound = softmax_of(q.double().cpu().numpy(), k, v, sk, sv, P, scale)
+    assert bound.max() < 0.01 * want.min()       # the bound is relative to the output itself
+    close(out, want, bound, torch.float32)
+    np.testing.assert_allclose(lse.double().cpu().numpy(), wlse, atol=2e-5, rtol=2e-6)
+    c.close()
+
 
 def test_attend_sums_of_pages_of_zero_values():
     """2,200,000 keys whose values are all zero: zeros, and the logarithm of a sum that keeps within fp32."""

@@ -20,11 +20,15 @@
 //    prompt with eight queries a key head: 512) the products bound it, and
 //    these MMAs reach 170 TFLOP/s there, a tenth of the tensor peak.
 //  - Scales never touch the codes: sk multiplies the finished score, sv enters
-//    the exponent.  With w_j = e^(z_j - M) sv and M a reference near the maximum
-//    of z_j + ln sv, the weights stay in (0, 256] whatever the pages' scales
-//    are; the sum of the softmax gets w_j / sv.  w_j is rounded to f16 for the
-//    value product (at most 2^-11 of it: the products run at the f16 rate and
-//    the error averages over the keys); all sums and statistics are fp32.
+//    the exponent.  With w_j = e^(z_j - M) sv and M a reference 2^11 to 2^15 below
+//    the maximum of z_j + ln sv, the weights stay in (0, 2^15] whatever the pages'
+//    scales are; the sum of the softmax gets w_j / sv.  w_j is rounded to f16 for
+//    the value product: at most 2^-11 of it (the products run at the f16 rate and
+//    the error averages over the keys), and below 2^-14 a step of 2^-24, which is
+//    at most 2^-36 of the largest weight for each key.  (M at the maximum itself
+//    left the upper half of f16's range unused: beside one key 18 nats above
+//    131,071 others the step was larger than their weights.)  All sums and
+//    statistics are fp32.
 //  - One warp of a CTA walks the work, looks pages and scales up, 32 steps at a
 //    time, one a lane, and copies each step's codes (TMA, swizzled: both
 //    ldmatrix patterns are free of bank conflicts) into a ring in shared
@@ -61,7 +65,7 @@ struct AttendParams {
     void *out;                         // [T][Hq][D]
     float *lse;                        // [T][Hq] or null
     float *part;                       // [2 grid][rows][D] unnormalised outputs of shared items
-    float2 *part_ml;                   // [2 grid][rows] maximum (base 2) and sum
+    float2 *part_ml;                   // [2 grid][rows] reference (base 2) and sum
     int *counters;                     // [3][grid], zero between calls
     int *status;
     int Hq, H, G;                      // query heads, key heads, queries a key head
@@ -145,7 +149,6 @@ __device__ __forceinline__ float at_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
 // Four codes -> two pairs of f16: neighbours (b0 b1, b2 b3: dimensions of a
 // key) or every other (b0 b2, b1 b3: a dimension of two tokens' values).
 // (Leaving int8 values 1152 too large and taking 1152 times the sum of the
@@ -375,7 +378,7 @@ constexpr int kAtTurn = 2;             // steps copied at a time (divides 8)
 constexpr int kAtSmemPerSm = 228 * 1024;
 constexpr int kAtSegment = 8;          // parts that are joined at a time
 // A page of zeros counts as one of a very small value scale, so that it leaves the reference to the others: weights over
-// that scale are as large as 2^108, and 2^20 of them would leave fp32.  The sums are kept 2^20 times smaller.
+// that scale are as large as 2^115, and 2^13 of them would leave fp32.  The sums are kept 2^20 times smaller.
 constexpr float kAtLeastScale = 1e-30f, kAtSumScale = 9.5367431640625e-07f, kAtLog2SumScale = -20.f;
 
 template <int D, int NT, int WARPS, int CTAS>
@@ -621,7 +624,9 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
 
     // ---------------------------------------------------- the working warps
     const int g = lane >> 2, c = lane & 3, tid = threadIdx.x;      // tid < 32 * WARPS
-    constexpr float kLog2e = 1.4426950408889634f, kLag = 8.f;
+    // the reference trails the largest score by kLift when it moves and by kLift + kLag, 2^15, at most (8 and 7, 4 and
+    // 11, 2 and 13 take 102.4, 102.5 and 103.0 us on 64 tokens over 8191)
+    constexpr float kLog2e = 1.4426950408889634f, kLag = 4.f, kLift = 11.f;
     const float zscale = p.cap > 0.f ? p.scale / p.cap : p.scale * kLog2e;
     const float zcap = p.cap * kLog2e;
 
@@ -777,15 +782,15 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) grows |= mx[nt][e] > m[nt][e] + kLag;
-            // The reference moves only when a score passes it by 2^8 (weights stay below 256): rescaling the sums is as
-            // much work as a step's softmax.
+                for (int e = 0; e < 2; ++e) grows |= mx[nt][e] - m[nt][e] > kLift + kLag;
+            // The reference moves only when a score passes the one that set it by 2^4: rescaling the sums is as much
+            // work as a step's softmax.  (The difference is the weights' exponent, so none of them passes 2^15.)
             if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float mn = fmaxf(m[nt][e], mx[nt][e]), f = mn == -INFINITY ? 1.f : at_exp2(m[nt][e] - mn);
+                        const float mn = fmaxf(m[nt][e], mx[nt][e] - kLift), f = mn == -INFINITY ? 1.f : at_exp2(m[nt][e] - mn);
                         l[nt][e] *= f;             // 0 for the first keys
 #pragma unroll
                         for (int ch = 0; ch < kChunks; ++ch) {
