@@ -148,3 +148,24 @@ def test_attend_sums_of_pages_of_zero_values():
     # of the 2^-24 of exponents near 100 that a logarithm, a score and the reference lose each, and some 100 fp32 sums
     assert abs(float(torch.logsumexp(z, 0)) - float(lse)) <= 3e-5
     c.close()
+
+
+def test_attend_counts_keys_of_zero_pages_beside_others():
+    """One page of values, hundreds of zeros: the zeros' keys are all of the sum's tail."""
+    P, D, n = 256, 64, 200000
+    pages = -(-n // P)
+    c = eva_vq.KVCache(1, 1, D, num_pages=pages, max_seqs=1, max_pages=pages, page_size=P, out_dtype="float32")
+    c.k[0, 0, 0, 0] = 127
+    c.v[0, 0] = 1
+    c.v_scale[0, 0] = 1.0
+    c.k_scale.fill_(0.03125)
+    q = torch.zeros((1, 1, D), dtype=torch.float16, device="cuda")
+    q[..., 0] = 40.0
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages)
+    lse = torch.empty((1, 1), device="cuda")
+    out = c.attend(q, i32([0, 1]), i32([n]), table, lse=lse)
+    top = 127 * 0.03125 * 40.0 * D ** -0.5
+    want = (np.exp(0.0) + 255 * np.exp(-top)) / (np.exp(0.0) + (n - 1) * np.exp(-top))
+    assert c.status() == eva_vq.EVA_OK
+    assert abs(float(out[0, 0, 0]) - want) <= 1e-5 and abs(float(lse) - (top + np.log1p((n - 1) * np.exp(-top)))) <= 1e-5
+    c.close()

@@ -149,6 +149,10 @@ __device__ __forceinline__ float at_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^(x / 2).  Sums are brought to another reference by two such factors: over pages of zeros they are up to 2^100 times
+// larger than their weights, and 2^x alone would be 0 for what still counts.
+__device__ __forceinline__ float at_half_exp2(float x) { return at_exp2(0.5f * x); }
+
 // Four codes -> two pairs of f16: neighbours (b0 b1, b2 b3: dimensions of a
 // key) or every other (b0 b2, b1 b3: a dimension of two tokens' values).
 // (Leaving int8 values 1152 too large and taking 1152 times the sum of the
@@ -790,8 +794,9 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float mn = fmaxf(m[nt][e], mx[nt][e] - kLift), f = mn == -INFINITY ? 1.f : at_exp2(m[nt][e] - mn);
-                        l[nt][e] *= f;             // 0 for the first keys
+                        const float mn = fmaxf(m[nt][e], mx[nt][e] - kLift);
+                        const float hf = mn == -INFINITY ? 1.f : at_half_exp2(m[nt][e] - mn), f = hf * hf;
+                        l[nt][e] = l[nt][e] * hf * hf;     // 0 for the first keys
 #pragma unroll
                         for (int ch = 0; ch < kChunks; ++ch) {
                             o[nt][ch][e] *= f;
@@ -918,10 +923,10 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
 #pragma unroll
                 for (int w = 0; w < WARPS; ++w) {
                     const float2 ml = mls[w * kRows + r];
-                    const float f = at_exp2(ml.x - ref);
+                    const float hf = at_half_exp2(ml.x - ref), f = hf * hf;
                     const float4 y = *reinterpret_cast<const float4 *>(os + (size_t)(w * kRows + r) * S::kOStride + x);
                     v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
-                    ll += ml.y * f;
+                    ll += ml.y * hf * hf;
                 }
                 if (c0 == c1) {
                     emit(r, x, v, mm, ll);
@@ -983,9 +988,9 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                             }
 #pragma unroll
                             for (int j = 0; j < kBatch; ++j) {
-                                const float f = cb + j * by <= to ? at_exp2(ml[j].x - ref) : 0.f;
+                                const float hf = cb + j * by <= to ? at_half_exp2(ml[j].x - ref) : 0.f, f = hf * hf;
                                 v.x += y[j].x * f; v.y += y[j].y * f; v.z += y[j].z * f; v.w += y[j].w * f;
-                                ll += ml[j].y * f;
+                                ll += ml[j].y * hf * hf;
                             }
                         }
                         if (final) {
