@@ -492,7 +492,8 @@ EVA_API eva_status_t eva_kv_create(eva_kv_t *out, const eva_kv_desc *desc, void 
  *               of n is at position lens[b] - n + i
  *   page_table  device int32 [B][max_pages]: page of positions
  *               [j page_size, (j + 1) page_size) of sequence b at [b][j]; entries
- *               behind its length are not read
+ *               behind its length are not read, nor by eva_kv_attend those wholly
+ *               before the windows of all its rows
  * A length or row range that cannot be right drops its sequence, a page outside
  * [0, num_pages) drops its tokens (they count as masked), and eva_kv_sync_status then returns
  * EVA_ERR_BAD_INDEX.

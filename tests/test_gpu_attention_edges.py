@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests import attn_reference as ref
 from tests.conftest import cuda_available
 from tests.test_gpu_attention import close, codes, cuda, i32, rng
 from vector_quantized_weight_b200 import eva_vq
@@ -129,6 +130,54 @@ def test_attend_keeps_the_tail_beside_a_dominating_key(cache, P, Hq, D, total, n
     close(out, want, bound, torch.float32)
     np.testing.assert_allclose(lse.double().cpu().numpy(), wlse, atol=2e-5, rtol=2e-6)
     c.close()
+
+
+@pytest.mark.parametrize("cache", ["int8", "e4m3"])
+@pytest.mark.parametrize("P,D,window,lens,n", [
+    (16, 64, 20, [70, 100, 37, 129], [1, 1, 1, 1]), (16, 128, 33, [97, 80, 64, 33], [1, 1, 1, 1]),
+    (16, 128, 17, [200, 48, 90], [3, 20, 9]), (16, 64, 1, [47, 48, 49, 33], [1, 1, 1, 1]),
+    (16, 256, 20, [70, 100, 37], [1, 4, 1]), (32, 128, 20, [70, 100, 37], [1, 4, 1]), (128, 64, 40, [300, 129], [1, 2]),
+])
+def test_attend_leaves_released_pages_alone(cache, P, D, window, lens, n):
+    """Pages wholly before the window of every row may be gone from the table, or hold another sequence's tokens by now
+    (here: a page of NaN codes, or of bytes with every bit set, and scales that are NaN)."""
+    Hq, H = 4, 2
+    r = rng(P + D + window)
+    used = [-(-x // P) for x in lens]
+    num_pages, width = sum(used) + 1, max(used)
+    free = num_pages - 1                         # the page that stands for what the released ones hold by now
+    first = [max(0, x - m + 1 - window) // P for x, m in zip(lens, n)]
+    gone, other = np.full((len(lens), width), -1), np.full((len(lens), width), -1)
+    at = 0
+    for b, u in enumerate(used):
+        gone[b, :u] = other[b, :u] = np.arange(at, at + u)
+        gone[b, :first[b]], other[b, :first[b]] = -1, free
+        at += u
+    raw = [r.integers(-100, 101, (num_pages, H, P, D)).astype(np.int8) for _ in range(2)]
+    for x in raw:
+        if cache == "e4m3":
+            x[(x & 127) == 127] = 3
+        x[free] = -1 if cache == "int8" else 127
+    kind = torch.int8 if cache == "int8" else torch.float8_e4m3fn
+    scales = [(0.5 + r.random((num_pages, H))) / (50 if cache == "int8" else 200) for _ in range(2)]
+    ts, ss = [cuda(x).view(kind) for x in raw], [cuda(x, torch.float32) for x in scales]
+    for s in ss:
+        s[free] = float("nan")
+    c = eva_vq.KVCache(Hq, H, D, num_pages=num_pages, max_seqs=len(lens), max_pages=width, page_size=P, dtype=cache, window=window,
+                       k=ts[0], v=ts[1], k_scale=ss[0], v_scale=ss[1])
+    starts = np.concatenate([[0], np.cumsum(n)])
+    q = cuda(r.standard_normal((int(starts[-1]), Hq, D)), torch.float16)
+    want, _, bound = ref.attend(q.double().cpu().numpy(), np.nan_to_num(codes(c.k)), scales_of(c.k_scale), np.nan_to_num(codes(c.v)),
+                                scales_of(c.v_scale), starts, lens, np.where(gone < 0, free, gone), window=window)
+    for table in (gone, other):
+        out = c.attend(q, i32(starts), i32(lens), i32(table))
+        assert c.status() == eva_vq.EVA_OK
+        close(out, want, bound, torch.float16)
+    c.close()
+
+
+def scales_of(t):
+    return t.nan_to_num(1.0).double().cpu().numpy()
 
 
 def test_attend_sums_of_pages_of_zero_values():

@@ -466,28 +466,31 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
             const int s_first = walk.tile.s0 + lo, n = hi - lo;
             if (n > 0) {
                 const int32_t *table = p.tok.table + (long long)walk.b * p.tok.max_pages;
+                // (a step of two pages may begin with one that is wholly before the window: gone, maybe, and not looked at)
+                const int seen = split && p.window > 0 ? walk.seq.len - walk.seq.n + walk.rt * kRows / p.G - p.window + 1 : 0;
+                auto there = [&](int tok) { return tok < walk.seq.len && tok + 16 > seen; };
                 int pid[2] = {-1, -1}, pid_next[2];        // pages of this lane's step, -1: no token there
                 auto look = [&](int s, int (&id)[2]) {
                     id[0] = id[1] = -1;
                     if (s >= n) return;
                     const int tok0 = (s_first + s) * kStep;
-                    if (tok0 < walk.seq.len) id[0] = table[tok0 >> p.tok.log_page];
-                    if (MT > 1 && tok0 + 16 < walk.seq.len) id[1] = split ? table[(tok0 >> p.tok.log_page) + 1] : id[0];
+                    if (there(tok0)) id[0] = table[tok0 >> p.tok.log_page];
+                    if (MT > 1 && there(tok0 + 16)) id[1] = split ? table[(tok0 >> p.tok.log_page) + 1] : id[0];
                 };
                 auto check = [&](int s, int (&id)[2]) {    // a page outside the cache: no token there, and say so
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         if (id[i] >= 0 && id[i] < p.tok.num_pages) continue;
-                        if (s < n && (s_first + s) * kStep + 16 * i < walk.seq.len) bad = true;
+                        if (s < n && there((s_first + s) * kStep + 16 * i)) bad = true;
                         id[i] = -1;
                     }
                 };
                 auto scale = [&](const int (&id)[2], float (&k)[2], float (&v)[2]) {
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        const bool there = id[i] >= 0;
-                        k[i] = there ? p.k_scale[(long long)id[i] * p.H + walk.h] : -1.f;
-                        v[i] = there ? p.v_scale[(long long)id[i] * p.H + walk.h] : 1.f;
+                        const bool in = id[i] >= 0;
+                        k[i] = in ? p.k_scale[(long long)id[i] * p.H + walk.h] : -1.f;
+                        v[i] = in ? p.v_scale[(long long)id[i] * p.H + walk.h] : 1.f;
                     }
                 };
                 auto copy = [&](int s, int stage) {        // this lane's step s into a stage
