@@ -467,7 +467,7 @@ typedef struct {
     int32_t cache_dtype;        /* eva_cache_dtype_t                                      */
     eva_dtype_t out_dtype;      /* of the attention output                                */
     int32_t window;             /* 0: every earlier key; w: the last w keys, itself included */
-    float softcap;              /* 0: none; c: scores become c tanh(score / c)            */
+    float softcap;              /* 0: none; c up to 1e30: scores become c tanh(score / c) */
     float scale;                /* of the scores; 0: 1 / sqrt(head_dim)                   */
 } eva_kv_desc;
 

@@ -132,6 +132,26 @@ def test_attend_keeps_the_tail_beside_a_dominating_key(cache, P, Hq, D, total, n
     c.close()
 
 
+@pytest.mark.parametrize("softcap", [5.0, 50.0, 1e3, 1e5, 1e9, 1e30])
+@pytest.mark.parametrize("cache,P,Hq,D,total,n", [("int8", 64, 4, 128, 700, 1), ("e4m3", 16, 2, 256, 300, 3), ("int8", 32, 8, 64, 500, 5)])
+def test_attend_with_small_and_large_caps(cache, P, Hq, D, total, n, softcap):
+    """A cap far above the scores leaves them as they are: the error is relative to the score, not to the cap."""
+    r = rng(total)
+    pages = -(-total // P)
+    k = ref.encode(ref.f32(r.standard_normal((total, 1, D)) * 30), cache)
+    v = ref.encode(ref.f32(r.standard_normal((total, 1, D)) * 30), cache)
+    sk, sv = (ref.f32((0.5 + r.random((pages, 1))) / 30) for _ in range(2))
+    q = cuda(2 * r.standard_normal((n, Hq, D)), torch.float16)
+    c, table = one_sequence(cache, P, Hq, k, v, sk, sv, softcap=softcap, out_dtype="float32")
+    lse = torch.empty((n, Hq), device="cuda")
+    out = c.attend(q, i32([0, n]), i32([total]), table, lse=lse)
+    assert c.status() == eva_vq.EVA_OK
+    want, wlse, bound = softmax_of(q.double().cpu().numpy(), k, v, sk, sv, P, D ** -0.5, softcap)
+    close(out, want, bound, torch.float32)
+    np.testing.assert_allclose(lse.double().cpu().numpy(), wlse, atol=2e-5, rtol=8e-6)
+    c.close()
+
+
 @pytest.mark.parametrize("cache", ["int8", "e4m3"])
 @pytest.mark.parametrize("P,D,window,lens,n", [
     (16, 64, 20, [70, 100, 37, 129], [1, 1, 1, 1]), (16, 128, 33, [97, 80, 64, 33], [1, 1, 1, 1]),

@@ -148,6 +148,7 @@ eva_status_t validate_kv(const eva_kv_desc *d) {
     if (d->cache_dtype != EVA_CACHE_INT8 && d->cache_dtype != EVA_CACHE_E4M3) return EVA_ERR_INVALID_ARG;
     if (!valid_dtype(d->out_dtype) || d->window < 0 || d->window > (1 << 30)) return EVA_ERR_INVALID_ARG;
     if (!(std::isfinite(d->softcap) && d->softcap >= 0) || !(std::isfinite(d->scale) && d->scale >= 0)) return EVA_ERR_INVALID_ARG;
+    if (d->softcap > 1e30f) return EVA_ERR_UNSUPPORTED;        // scores over it would be subnormal
     if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return EVA_ERR_UNSUPPORTED;
     if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128 && d->page_size != 256)
         return EVA_ERR_UNSUPPORTED;
