@@ -539,12 +539,13 @@ EVA_API eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const
                                    eva_stream_t stream);
 
 /* Synchronises the device, reports and clears the handle's error word:
- * EVA_ERR_BAD_INDEX (above) or EVA_ERR_DEVICE_TIMEOUT (a bounded wait gave up; that
- * call's outputs are undefined). */
+ * EVA_ERR_BAD_INDEX (above) or EVA_ERR_DEVICE_TIMEOUT (a bounded wait gave up: the outputs of that
+ * call and of the handle's later ones, up to this, are undefined). */
 EVA_API eva_status_t eva_kv_sync_status(eva_kv_t h);
 
 /* Failure-detection test hook: the next eva_kv_attend streams nothing, so that its waits
- * run out after `rounds` tries (1 .. 2^20).  One-shot; its outputs are undefined. */
+ * run out after `rounds` tries (1 .. 2^20); or, with -rounds, its working warps give up at once
+ * beside the stream.  One-shot; its outputs are undefined. */
 EVA_API eva_status_t eva_kv_debug_inject_wait_timeout(eva_kv_t h, int32_t rounds);
 
 typedef struct {

@@ -6,7 +6,7 @@ import torch
 
 from tests import attn_reference as ref
 from tests.conftest import cuda_available
-from tests.test_gpu_attention import close, codes, cuda, i32, rng
+from tests.test_gpu_attention import close, codes, cuda, i32, make_cache, rng
 from vector_quantized_weight_b200 import eva_vq
 
 pytestmark = [pytest.mark.gpu,
@@ -238,3 +238,24 @@ def test_attend_counts_keys_of_zero_pages_beside_others():
     assert c.status() == eva_vq.EVA_OK
     assert abs(float(out[0, 0, 0]) - want) <= 1e-5 and abs(float(lse) - (top + np.log1p((n - 1) * np.exp(-top)))) <= 1e-5
     c.close()
+
+
+# ------------------------------------------------------------------ the cache
+
+def test_attend_gives_up_with_copies_in_flight():
+    """The working warps give up at once while the streaming warp fills the ring: the call ends with the status, and what
+    follows eva_kv_sync_status is right."""
+    for cache, P, Hq, H, D, lens, n in (("int8", 64, 16, 2, 128, [3000, 20], [1, 1]), ("e4m3", 16, 8, 4, 64, [2000], [5]),
+                                        ("int8", 32, 4, 2, 256, [1500, 900], [1, 1]), ("int8", 64, 8, 1, 128, [4000], [40])):
+        c, table = make_cache(cache, lens, P, H, D, 131, Hq=Hq)
+        starts = np.concatenate([[0], np.cumsum(n)])
+        q = cuda(rng(132).standard_normal((int(starts[-1]), Hq, D)), torch.float16)
+        args = (q, i32(starts), i32(lens), i32(table))
+        good = c.attend(*args)
+        assert c.status() == eva_vq.EVA_OK
+        for _ in range(3):
+            eva_vq.eva_kv_debug_inject_wait_timeout(c.handle, -64)
+            c.attend(*args)
+            assert c.status() == eva_vq.EVA_ERR_DEVICE_TIMEOUT
+            assert torch.equal(c.attend(*args), good) and c.status() == eva_vq.EVA_OK
+        c.close()

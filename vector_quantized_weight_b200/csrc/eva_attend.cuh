@@ -70,7 +70,7 @@ struct AttendParams {
     int *status;
     int Hq, H, G;                      // query heads, key heads, queries a key head
     int window, out_f32, min_steps, wait_rounds;
-    int inject;                        // test hook: stream nothing, so that every wait runs out
+    int inject;                        // test hook, 1: stream nothing, so that every wait runs out; 2: work on nothing
     float scale, cap;                  // cap 0: none
 };
 
@@ -124,15 +124,6 @@ __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, int round
         : "r"(bar), "r"(parity), "r"(rounds)
         : "memory");
     return ok != 0;
-}
-// A counter in shared memory that one warp advances and the others read.
-__device__ __forceinline__ void at_publish(uint32_t a, int v) {
-    asm volatile("st.release.cta.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ int at_published(uint32_t a) {
-    int v;
-    asm volatile("ld.acquire.cta.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
 }
 __device__ __forceinline__ uint32_t at_transpose(uint32_t x) {
     uint32_t y;
@@ -464,6 +455,8 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
         const bool split = page < kStep;                   // a step's halves lie on two pages
         const int box = split ? 16 : kStep;
         int t = 0, st = 0, ahead = 0;  // steps so far, the next one's stage, steps copied before their scales were known
+        int landed = 0;                // of the last steps, where the warp gave up
+        auto land = [&](int step) { mbar_wait_bounded(full_a + 8 * (step % kStages), (step / kStages) & 1, kWaitRounds); };
         uint32_t parity = 1;           // of the free barriers: the first round passes at once
         int ps = 0, handed = 0;        // the next piece's place, pieces so far
         int used0 = kRows, used1 = kRows;      // rows of each place's queries that may not be zeros
@@ -522,7 +515,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 };
                 look(lane, pid);
                 check(lane, pid);
-                if (t == 0 && !p.inject) {
+                if (t == 0 && p.inject != 1) {
                     ahead = min(min(n, 32), kStages);
                     if (lane < ahead) copy(lane, lane);
                 }
@@ -568,7 +561,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                     ps = 0;
                     pparity ^= 1;
                 }
-                ok = !p.inject;
+                ok = p.inject != 1;
                 for (int s0 = 0; s0 < n && ok; s0 += 32) {
                     look(s0 + 32 + lane, pid_next);        // in flight while these steps go out
                     AtScales sc = {};
@@ -597,7 +590,12 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                             }
                         }
                         ok = __all_sync(0xffffffffu, there);
-                        if (!ok) break;
+                        if (!ok) {             // the turn's stages hold these steps, or still those of a round before
+                            if (mine >= 0 && mine < turn) land(t + mine - (there ? 0 : kStages));
+                            t += turn;
+                            landed = turn;
+                            break;
+                        }
                         t += turn;
                         st += turn;
                         if (st >= kStages) {
@@ -625,15 +623,17 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
             mbar_arrive(pfull_a + 8 * ps);
         }
         if (bad) atomicOr(p.status, kKvStatusIndex);
-        if (!ok) {                     // another warp gave up: say so, let the copies in flight land
+        if (!ok) {                     // another warp gave up: say so
             if (lane == 0) atomicOr(p.status, kAtStatusWait);
             for (; t < ahead; ++t)
                 if (lane == 0) mbar_arrive(full_a + 8 * t);
-            for (int i = max(0, handed - kAtPieces); i < handed; ++i)
-                mbar_wait_bounded(pfull_a + 8 * (i % kAtPieces), (i / kAtPieces) & 1, p.wait_rounds);
-            for (int i = max(0, t - kStages); i < t; ++i)
-                mbar_wait_bounded(full_a + 8 * (i % kStages), (i / kStages) & 1, p.wait_rounds);
         }
+        // No copy outlives its CTA, whether or not the working warps are there to wait for it.  (Of the last two pieces the
+        // first is done with where the CTA's end was handed over in its place.)
+        const int piece = handed - 1 - lane, step = t - landed - 1 - lane;
+        if (piece >= 0 && lane < (ok ? kAtPieces - 1 : kAtPieces))
+            mbar_wait_bounded(pfull_a + 8 * (piece % kAtPieces), (piece / kAtPieces) & 1, kWaitRounds);
+        if (step >= 0 && lane < kStages - landed) land(step);
         return;
     }
 
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
     uint32_t pparity = 0, own_parity = 0;
     bool ok = true, first = true;
     for (;;) {
-        ok = at_wait(pfull_a + 8 * ps, pparity, p.wait_rounds);
+        ok = p.inject != 2 && at_wait(pfull_a + 8 * ps, pparity, p.wait_rounds);
         if (!ok) break;
         const AtPiece &bt = pieces[ps];
         const int t_end = bt.t0 + bt.n, step0 = bt.s_first - bt.t0;

@@ -516,8 +516,8 @@ eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t
     p.window = d.window;
     p.out_f32 = d.out_dtype == EVA_F32;
     p.min_steps = 16;
-    p.inject = h->inject_wait_rounds > 0;
-    p.wait_rounds = p.inject ? h->inject_wait_rounds : kWaitRounds;
+    p.inject = h->inject_wait_rounds > 0 ? 1 : h->inject_wait_rounds < 0 ? 2 : 0;
+    p.wait_rounds = p.inject ? std::abs(h->inject_wait_rounds) : kWaitRounds;
     h->inject_wait_rounds = 0;
     p.scale = d.scale > 0 ? d.scale : 1.0f / std::sqrt((float)d.head_dim);
     p.cap = d.softcap;
@@ -562,7 +562,7 @@ eva_status_t eva_kv_cache_info(eva_kv_t h, eva_kv_info *info) {
 }
 
 eva_status_t eva_kv_debug_inject_wait_timeout(eva_kv_t h, int32_t rounds) {
-    if (!h || rounds < 1 || rounds > kWaitRounds) return EVA_ERR_INVALID_ARG;
+    if (!h || rounds == 0 || rounds > kWaitRounds || rounds < -kWaitRounds) return EVA_ERR_INVALID_ARG;
     h->inject_wait_rounds = rounds;
     return EVA_OK;
 }
