@@ -486,8 +486,8 @@ EVA_API eva_status_t eva_kv_create(eva_kv_t *out, const eva_kv_desc *desc, void 
 /*
  * Common to the next three calls: T packed rows of B sequences, 1 <= B <= max_seqs.
  *   starts      device int32 [B + 1]: sequence b has rows starts[b] .. starts[b+1] - 1
- *               (non-decreasing, at most T); rows behind starts[B] are neither
- *               read nor written, so a padded batch may leave some
+ *               (non-decreasing, at most T); rows before starts[0] and behind starts[B] are
+ *               neither read nor written, so a padded batch may leave some
  *   lens        device int32 [B]: each sequence's length WITH those rows: row i
  *               of n is at position lens[b] - n + i
  *   page_table  device int32 [B][max_pages]: page of positions
@@ -516,7 +516,7 @@ EVA_API eva_status_t eva_kv_append(eva_kv_t h, const void *k, int64_t ldk, const
 /*
  * The stored values back: rows starts[b] .. of k_out and v_out ([T][kv_heads][head_dim] of out_dtype,
  * contiguous; either may be NULL) are the tokens at positions begins[b] ..
- * of sequence b.
+ * of sequence b.  A position behind the table's last column is dropped like a page outside the cache.
  */
 EVA_API eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_t *begins, const int32_t *page_table,
                                  int32_t B, int32_t T, eva_dtype_t out_dtype, void *k_out, void *v_out,

@@ -242,6 +242,35 @@ def test_attend_counts_keys_of_zero_pages_beside_others():
 
 # ------------------------------------------------------------------ the cache
 
+def test_read_leaves_rows_of_no_sequence_and_drops_ranges_that_cannot_be_right():
+    H, D, P = 2, 64, 16
+    c, table = make_cache("int8", [40, 33], P, H, D, 121)
+    values = codes(c.k)[:, :, :, :] * c.k_scale.double().cpu().numpy()[..., None, None]
+
+    def token(b, pos):
+        return ref.f32(values[table[b][pos // P], :, pos % P])
+
+    def read(starts, begins, rows):
+        k, v = (torch.full((rows, H, D), 7.0, device="cuda") for _ in range(2))
+        c.read(i32(starts), i32(begins), i32(table), rows, k_out=k, v_out=v, dtype="float32")
+        return k.cpu().numpy(), c.status()
+
+    # rows before the first sequence and behind the last are nobody's
+    k, st = read([2, 5, 7], [10, 20], 9)
+    assert st == eva_vq.EVA_OK
+    for row, (b, pos) in {2: (0, 10), 3: (0, 11), 4: (0, 12), 5: (1, 20), 6: (1, 21)}.items():
+        np.testing.assert_array_equal(k[row], token(b, pos))
+    assert np.all(k[[0, 1, 7, 8]] == 7.0)
+    # a range that goes backwards, past the rows, or begins before them drops its sequence, no other
+    for starts, begins, kept in (([0, 2, 0], [10, 20], {0: (0, 10), 1: (0, 11)}), ([0, 2, 99], [10, 20], {0: (0, 10), 1: (0, 11)}),
+                                 ([-1, 2, 4], [10, 20], {2: (1, 20), 3: (1, 21)}), ([0, 2, 4], [-3, 20], {2: (1, 20), 3: (1, 21)})):
+        k, st = read(starts, begins, 4)
+        assert st == eva_vq.EVA_ERR_BAD_INDEX
+        for row in range(4):
+            np.testing.assert_array_equal(k[row], token(*kept[row]) if row in kept else np.full((H, D), 7.0))
+    c.close()
+
+
 def test_attend_gives_up_with_copies_in_flight():
     """The working warps give up at once while the streaming warp fills the ring: the call ends with the status, and what
     follows eva_kv_sync_status is right."""

@@ -19,7 +19,6 @@
 //  eva_kv_read_kernel    one warp per token (or 8 of them), keys or values
 #pragma once
 #include <cuda_fp16.h>
-#include <limits.h>
 #include <stdint.h>
 
 #include "eva_rope.cuh"
@@ -354,24 +353,39 @@ __global__ void __launch_bounds__(kKvThreads) eva_kv_read_kernel(KvReadParams p)
     pdl_launch();
     void *dst = kv ? p.out[1] : p.out[0];
     if (row0 >= p.tok.T || !dst) return;
-    // Lane r looks up row r of the warp.  Its sequence: how many of starts[1 .. B] are at or before it.
+    // Lane r looks up row r of the warp: the sequence whose range has it, if any.  A range that goes backwards or leaves
+    // the T rows has none.
     const int row = row0 + lane;
     const bool mine = lane < p.rows && row < p.tok.T;
-    int b = 0;
-    for (int b0 = 1; b0 <= p.tok.B; b0 += 32) {
-        const int at = b0 + lane <= p.tok.B ? p.tok.starts[b0 + lane] : INT_MAX;
+    int b = -1, first = 0;
+    bool bad = false;
+    for (int b0 = 0; b0 < p.tok.B; b0 += 32) {
+        int lo = 0, hi = 0;
+        if (b0 + lane < p.tok.B) {
+            lo = p.tok.starts[b0 + lane];
+            hi = p.tok.starts[b0 + lane + 1];
+            if (lo < 0 || hi < lo || hi > p.tok.T) {
+                bad = true;
+                hi = lo;
+            }
+        }
         for (int r = 0; r < p.rows; ++r) {
-            const int n = __popc(__ballot_sync(0xffffffffu, at <= row0 + r));
-            if (lane == r) b += n;
+            const unsigned who = __ballot_sync(0xffffffffu, lo <= row0 + r && row0 + r < hi);
+            const int src = who ? __ffs(who) - 1 : 0, at = __shfl_sync(0xffffffffu, lo, src);
+            if (lane == r && who && b < 0) {
+                b = b0 + src;
+                first = at;
+            }
         }
     }
+    if (bad) atomicOr(p.status, kKvStatusIndex);
     long long tile = -1;                 // (page, head 0), -1: nothing to read
     int slot = 0;
-    if (mine && b < p.tok.B) {           // rows behind the last sequence stay as they were
-        const int first = p.tok.starts[b], begin = p.tok.lens[b];
+    if (mine && b >= 0) {                // rows of no sequence stay as they were
+        const int begin = p.tok.lens[b];
         const long long pos = (long long)begin + row - first;
         int page = -1;
-        if (first >= 0 && row >= first && begin >= 0 && pos < (long long)p.tok.max_pages * p.tok.page) {
+        if (begin >= 0 && pos < (long long)p.tok.max_pages * p.tok.page) {
             page = p.tok.table[(long long)b * p.tok.max_pages + (pos >> p.tok.log_page)];
             slot = (int)(pos & (p.tok.page - 1));
         }
