@@ -527,7 +527,8 @@ EVA_API eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_
  * to the next, rows 16-byte aligned); out [T][q_heads][head_dim] of the descriptor's out_dtype,
  * contiguous; lse (optional) fp32 [T][q_heads], the natural logarithm of the sum of
  * exponentials.  The row at position p sees keys j <= p, with a window j > p - window.  A row that
- * sees no key gives zeros and lse = -infinity; what the buffers hold where no token is does not matter.  Statistics and sums are fp32; the
+ * sees no key gives zeros and lse = -infinity; what the buffers hold where no token is does not matter.  A query with
+ * a NaN gives NaN, in lse too, and leaves the other rows alone.  Statistics and sums are fp32; the
  * softmax weights (times their page's value scale) are rounded to fp16 for the value product: by at most
  * 2^-11 of themselves, or 2^-36 of the largest.  Results do not depend
  * on timing; they may differ in the last bits between batches, whose work is

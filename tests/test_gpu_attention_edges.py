@@ -240,6 +240,28 @@ def test_attend_counts_keys_of_zero_pages_beside_others():
     c.close()
 
 
+@pytest.mark.parametrize("D,Hq,n,total", [(128, 8, 1, 300), (64, 4, 4, 90), (256, 4, 1, 200), (128, 8, 12, 900)])
+def test_attend_keeps_a_nan_in_its_row(D, Hq, n, total):
+    c, table = make_cache("int8", [total], 64, 2, D, 111, Hq=Hq)
+    q = cuda(rng(112).standard_normal((n, Hq, D)), torch.float16)
+    args = (i32([0, n]), i32([total]), i32(table))
+    lse, lse2 = (torch.empty((n, Hq), device="cuda") for _ in range(2))
+    c.attend(q, *args, lse=lse)
+    want, _, bound = ref.attend(q.double().cpu().numpy(), codes(c.k), c.k_scale.double().cpu().numpy(), codes(c.v),
+                                c.v_scale.double().cpu().numpy(), [0, n], [total], table)
+    odd = q.clone()
+    odd[0, 1, 3], odd[n - 1, Hq - 1, 0] = float("nan"), float("inf")
+    out = c.attend(odd, *args, lse=lse2)
+    assert c.status() == eva_vq.EVA_OK
+    hit = torch.zeros((n, Hq), dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[n - 1, Hq - 1] = True
+    rest = ~hit.cpu().numpy()
+    close(out[~hit], want[rest], bound[rest], torch.float16)
+    assert float((lse2[~hit] - lse[~hit]).abs().max()) <= 1e-5
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse2[hit]).all()
+    c.close()
+
+
 # ------------------------------------------------------------------ the cache
 
 def test_read_leaves_rows_of_no_sequence_and_drops_ranges_that_cannot_be_right():

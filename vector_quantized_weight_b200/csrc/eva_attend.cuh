@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
                 }
                 if (p.lse && x == 0)
-                    p.lse[(long long)(erow + i) * p.Hq + hq] = ll > 0.f ? (mm + (log2f(ll) - kAtLog2SumScale)) * 0.6931471805599453f : -INFINITY;
+                    p.lse[(long long)(erow + i) * p.Hq + hq] = ll == 0.f ? -INFINITY : (mm + (log2f(ll) - kAtLog2SumScale)) * 0.6931471805599453f;
             };
 #pragma unroll 1
             for (int i = tid; i < erows * (D / 4); i += 32 * WARPS) {
