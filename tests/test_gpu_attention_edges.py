@@ -310,3 +310,12 @@ def test_attend_gives_up_with_copies_in_flight():
             assert c.status() == eva_vq.EVA_ERR_DEVICE_TIMEOUT
             assert torch.equal(c.attend(*args), good) and c.status() == eva_vq.EVA_OK
         c.close()
+
+
+def test_device_without_a_number_is_the_current_one():
+    dev = torch.device("cuda", torch.cuda.current_device())
+    c = eva_vq.KVCache(1, 1, 64, num_pages=1, max_seqs=1, max_pages=1, device="cuda")
+    rope = eva_vq.HeadRope(1, 1, 64, device="cuda")
+    assert c.device == dev and rope.device == dev and c.k.device == dev
+    c.close()
+    rope.close()

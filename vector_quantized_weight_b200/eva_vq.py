@@ -501,6 +501,15 @@ def _indices(name, x, shape, device):
                          f"not {x.dtype} {tuple(x.shape)} on {x.device}")
 
 
+def _cuda_device(device):
+    """A CUDA device with its number: the current one for None and for "cuda"."""
+    import torch
+    d = torch.device("cuda" if device is None else device)
+    if d.type != "cuda":
+        raise ValueError(f"the device must be a CUDA device, not {d}")
+    return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
 class _OnDevice:
     """A handle on one device: its stream, and outputs that belong to the stream of the call.  A decode step's calls
     are a few microseconds of device time, so what a call needs of torch is looked up once."""
@@ -564,7 +573,7 @@ class HeadRope(_OnDevice):
         unknown = set(how) - {"factor", "original", "low", "high", "magnitude"}
         if unknown:
             raise ValueError(f"unknown scaling entries {sorted(unknown)}")
-        self.device = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index or 0)
+        self.device = _cuda_device(device)
         for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
             if w is not None and (w.dtype != torch.float16 or w.device != self.device or
                                   tuple(w.shape) != (self.head_dim,) or not w.is_contiguous()):
@@ -640,9 +649,7 @@ class KVCache(_OnDevice):
         self.max_seqs, self.max_pages = int(max_seqs), int(max_pages)
         self.out_dtype, code_out = _dtype(out_dtype)
         given = [t for t in (k, v, k_scale, v_scale) if t is not None]
-        if device is None:
-            device = given[0].device if given else torch.device("cuda", torch.cuda.current_device())
-        self.device = torch.device("cuda", torch.device(device).index or 0)
+        self.device = _cuda_device(given[0].device if device is None and given else device)
         code_type = torch.int8 if dtype == "int8" else torch.float8_e4m3fn
         tile = (int(num_pages), self.kv_heads)
         made = []
