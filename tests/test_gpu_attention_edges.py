@@ -312,6 +312,25 @@ def test_attend_gives_up_with_copies_in_flight():
         c.close()
 
 
+def test_buffers_made_for_a_stream_are_ready_on_it():
+    """A cache made with stream=s fills its buffers on s: what s writes next is not overwritten by zeros that another,
+    busy stream still owes."""
+    H, D, P = 2, 64, 16
+    s = torch.cuda.Stream()
+    x = cuda(rng(141).standard_normal((5, H, D)), torch.float16)
+    starts, lens, table = i32([0, 5]), i32([5]), i32([[0]])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)               # about 0.1 s on the current stream
+    c = eva_vq.KVCache(H, H, D, num_pages=2, max_seqs=1, max_pages=1, page_size=P, stream=s)
+    c.append(x, x, starts, lens, table, stream=s)
+    torch.cuda.synchronize()
+    assert c.status() == eva_vq.EVA_OK
+    k, _ = c.read(starts, i32([0]), table, 5, dtype="float32")
+    assert float((k - x.float()).abs().max()) <= 0.51 * float(c.k_scale[0].max())
+    assert torch.all(c.k[1] == 0) and torch.all(c.k_scale[1] == 0)
+    c.close()
+
+
 def test_device_without_a_number_is_the_current_one():
     dev = torch.device("cuda", torch.cuda.current_device())
     c = eva_vq.KVCache(1, 1, 64, num_pages=1, max_seqs=1, max_pages=1, device="cuda")

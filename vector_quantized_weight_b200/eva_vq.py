@@ -656,8 +656,9 @@ class KVCache(_OnDevice):
         for name, t, shape, kind in (("k", k, tile + (int(page_size), self.head_dim), code_type),
                                      ("v", v, tile + (int(page_size), self.head_dim), code_type),
                                      ("k_scale", k_scale, tile, torch.float32), ("v_scale", v_scale, tile, torch.float32)):
-            if t is None:
-                t = torch.zeros(shape, dtype=kind, device=self.device)
+            if t is None:                      # on the stream that __init__ waits for: the first call may be on any other
+                with torch.cuda.stream(stream):
+                    t = torch.zeros(shape, dtype=kind, device=self.device)
             elif t.dtype != kind or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {kind} tensor {shape} on {self.device}")
             made.append(t)
