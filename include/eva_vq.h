@@ -534,6 +534,7 @@ EVA_API eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_
  * on timing; they may differ in the last bits between batches, whose work is
  * cut at other places.  The handle's workspace is shared: one handle must not attend on two
  * streams at once, captured graphs included (give each stream a handle over the same buffers).
+ * A call of more than 2^30 steps (32 tokens for 8 to 32 rows) a CTA writes nothing and gives EVA_ERR_BAD_INDEX.
  */
 EVA_API eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t *starts, const int32_t *lens,
                                    const int32_t *page_table, int32_t B, int32_t T, void *out, float *lse,

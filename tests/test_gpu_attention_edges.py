@@ -338,3 +338,16 @@ def test_device_without_a_number_is_the_current_one():
     assert c.device == dev and rope.device == dev and c.k.device == dev
     c.close()
     rope.close()
+
+
+def test_attend_refuses_more_steps_than_a_cta_counts():
+    """More than 300,000 rows at the end of a sequence of 2^30 tokens: nothing is read or written, and the status says so."""
+    P, D, n = 256, 64, 40000
+    c = eva_vq.KVCache(8, 1, D, num_pages=1, max_seqs=1, max_pages=1 << 22, page_size=P)
+    q = torch.zeros((n, 8, D), dtype=torch.float16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    table = torch.full((1, 1 << 22), -1, dtype=torch.int32, device="cuda")
+    c.attend(q, i32([0, n]), i32([1 << 30]), table, out=out)
+    assert c.status() == eva_vq.EVA_ERR_BAD_INDEX
+    assert torch.all(out == 7.0)
+    c.close()

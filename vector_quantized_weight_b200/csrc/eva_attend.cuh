@@ -273,6 +273,10 @@ struct AtWalk {
             total = steps + items * kAtItemCost;
             parts = (int)min((long long)grid, (total + p.min_steps - 1) / p.min_steps);
             if (c >= parts) return;
+            if (total / parts >= (1 << 30)) {  // a CTA counts its steps in 32 bits
+                bad = true;
+                return;
+            }
             place = total * c / parts;
             left = (int)(total * (c + 1) / parts - place);
         }
