@@ -200,6 +200,35 @@ def scales_of(t):
     return t.nan_to_num(1.0).double().cpu().numpy()
 
 
+@pytest.mark.parametrize("P,Hq,D,total,n", [
+    (64, 1, 128, 70001, 1),           # 137 parts of one item: segments of 16, the last of 9
+    (128, 8, 64, 131071, 1),          # 256 parts: 16 full segments
+    (64, 2, 128, 66000, 1),           # 129 parts: the last segment is one part
+    (32, 1, 256, 36000, 1),           # heads of 256: steps of 16 tokens, 141 parts
+    (64, 5, 128, 70001, 3),           # 15 rows: items of 16
+    (64, 16, 64, 50001, 9),           # many rows: several items, many parts each
+])
+@pytest.mark.parametrize("cache", ["int8", "e4m3"])
+def test_attend_joins_very_many_parts(cache, P, Hq, D, total, n):
+    r = rng(total + D)
+    pages = -(-total // P)
+    k = ref.encode(ref.f32(r.standard_normal((total, 1, D)) * 30), cache)
+    v = ref.encode(ref.f32(r.standard_normal((total, 1, D)) * 30 + 20), cache)
+    sk, sv = (ref.f32((0.5 + r.random((pages, 1))) / 30) for _ in range(2))
+    q = cuda(r.standard_normal((n, Hq, D)), torch.float16)
+    c, table = one_sequence(cache, P, Hq, k, v, sk, sv, out_dtype="float32")
+    lse = torch.empty((n, Hq), device="cuda")
+    args = (q, i32([0, n]), i32([total]), table)
+    out = c.attend(*args, lse=lse)
+    want, wlse, bound = softmax_of(q.double().cpu().numpy(), k, v, sk, sv, P, D ** -0.5)
+    close(out, want, bound, torch.float32)
+    np.testing.assert_allclose(lse.double().cpu().numpy(), wlse, atol=2e-5, rtol=2e-6)
+    for _ in range(20):
+        assert torch.equal(c.attend(*args), out)
+    assert c.status() == eva_vq.EVA_OK
+    c.close()
+
+
 def test_attend_sums_of_pages_of_zero_values():
     """2,200,000 keys whose values are all zero: zeros, and the logarithm of a sum that keeps within fp32."""
     P, D, total = 256, 64, 2200000
