@@ -438,7 +438,7 @@ EVA_API eva_status_t eva_rope_create(eva_rope_t *out, const eva_rope_desc *desc,
                                      const void *k_weight, eva_stream_t stream);
 
 /*
- * Norm and turn T tokens' heads in one pass.  q: [T][q_heads][head_dim], ldq
+ * Norm and turn T (at most 2^30) tokens' heads in one pass.  q: [T][q_heads][head_dim], ldq
  * elements from one token to the next (at least q_heads * head_dim, so q may be
  * a column range of a fused projection's rows); k, q_out, k_out likewise.
  * positions: device int32 [T], any value (NULL when rotary_dim is 0).  Angles are
@@ -484,7 +484,7 @@ EVA_API eva_status_t eva_kv_create(eva_kv_t *out, const eva_kv_desc *desc, void 
                                    float *v_scale, eva_stream_t stream);
 
 /*
- * Common to the next three calls: T packed rows of B sequences, 1 <= B <= max_seqs.
+ * Common to the next three calls: T (at most 2^30) packed rows of B sequences, 1 <= B <= max_seqs.
  *   starts      device int32 [B + 1]: sequence b has rows starts[b] .. starts[b+1] - 1
  *               (non-decreasing, at most T); rows before starts[0] and behind starts[B] are
  *               neither read nor written, so a padded batch may leave some
@@ -534,7 +534,7 @@ EVA_API eva_status_t eva_kv_read(eva_kv_t h, const int32_t *starts, const int32_
  * on timing; they may differ in the last bits between batches, whose work is
  * cut at other places.  The handle's workspace is shared: one handle must not attend on two
  * streams at once, captured graphs included (give each stream a handle over the same buffers).
- * A call of more than 2^30 steps (32 tokens for 8 to 32 rows) a CTA writes nothing and gives EVA_ERR_BAD_INDEX.
+ * A call of more than 2^30 steps a CTA (8 to 32 rows over 32 tokens, heads of 256: 16) writes nothing and gives EVA_ERR_BAD_INDEX.
  */
 EVA_API eva_status_t eva_kv_attend(eva_kv_t h, const void *q, int64_t ldq, const int32_t *starts, const int32_t *lens,
                                    const int32_t *page_table, int32_t B, int32_t T, void *out, float *lse,
@@ -553,7 +553,7 @@ EVA_API eva_status_t eva_kv_debug_inject_wait_timeout(eva_kv_t h, int32_t rounds
 typedef struct {
     int64_t workspace_bytes;
     int32_t sm_count;
-    int32_t rows, grid, stages; /* last attention call: rows an item, CTAs, steps of 32 tokens in flight a CTA */
+    int32_t rows, grid, stages; /* last attention call: rows an item, CTAs, steps in flight a CTA (of 32 tokens, heads of 256: 16) */
 } eva_kv_info;
 EVA_API eva_status_t eva_kv_cache_info(eva_kv_t h, eva_kv_info *info);
 

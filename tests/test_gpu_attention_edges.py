@@ -380,3 +380,12 @@ def test_attend_refuses_more_steps_than_a_cta_counts():
     assert c.status() == eva_vq.EVA_ERR_BAD_INDEX
     assert torch.all(out == 7.0)
     c.close()
+
+
+def test_calls_of_more_than_a_billion_rows_are_refused():
+    rope = eva_vq.HeadRope(1, 1, 2)
+    lib, x = eva_vq.load(), torch.zeros((4, 2), dtype=torch.float16, device="cuda")
+    P = x.data_ptr()
+    for T in ((1 << 30) + 1, (1 << 31) - 1, -1):
+        assert lib.eva_rope_run(rope.handle, P, 2, P, 2, P, T, P, 2, P, 2, None) == eva_vq.EVA_ERR_INVALID_ARG
+    rope.close()

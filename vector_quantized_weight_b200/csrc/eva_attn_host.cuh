@@ -321,7 +321,7 @@ eva_status_t eva_rope_create(eva_rope_t *out, const eva_rope_desc *desc, const v
 
 eva_status_t eva_rope_run(eva_rope_t h, const void *q, int64_t ldq, const void *k, int64_t ldk, const int32_t *positions,
                           int32_t T, void *q_out, int64_t ldqo, void *k_out, int64_t ldko, eva_stream_t stream) {
-    if (!h || T < 0) return EVA_ERR_INVALID_ARG;
+    if (!h || T < 0 || T > (1 << 30)) return EVA_ERR_INVALID_ARG;
     if (T == 0) return EVA_OK;
     const eva_rope_desc &d = h->desc;
     if (d.rotary_dim && !positions) return EVA_ERR_INVALID_ARG;
