@@ -18,7 +18,7 @@
 //    eight rows the tensor pipe is 11 % busy at full stream speed and the
 //    conversion into registers is the work.  With many rows (64 tokens of a
 //    prompt with eight queries a key head: 512) the products bound it, and
-//    these MMAs reach 170 TFLOP/s there, a tenth of the tensor peak.
+//    these MMAs reach 169 TFLOP/s there, a tenth of the tensor peak.
 //  - Scales never touch the codes: sk multiplies the finished score, sv enters
 //    the exponent.  With w_j = e^(z_j - M) sv and M a reference 2^11 to 2^15 below
 //    the maximum of z_j + ln sv, the weights stay in (0, 2^15] whatever the pages'
@@ -42,10 +42,10 @@
 //    is joined by the last of them to finish, in the order of the parts, so
 //    results do not depend on timing.
 //
-// Measured (device time): 268 MB of cache as 64 sequences 58 us (4.7 TB/s), as
+// Measured (device time): 268 MB of cache as 64 sequences 59 us (4.5 TB/s), as
 // one 54 us (5.0 TB/s, of which 39 us stream at the memory's rate and the rest
 // is the start's three dependent lookups, the joins and the slowest CTAs); 517
-// tokens of 32 heads 10.1 us, all of it latency.
+// tokens of 32 heads 10.3 us, all of it latency.
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>

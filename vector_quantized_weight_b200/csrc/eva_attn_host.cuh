@@ -183,8 +183,10 @@ cudaError_t plan_attend(eva_kv *h, int i, int optin) {
 }
 // Warps and CTAs an SM, all measured (us, 517 tokens of 32 heads / 268 MB of 64 sequences / of one): for up to eight
 // rows two CTAs of 5 working warps 10.7 / 57.8 / 54.3, three of 4 11.7 / 55.5 / 54.0, two of 4 11.0 / 58.4 / 54.5,
-// four of 3 12.6 / 56.7 / 57.5, two of 7 11.5 / 61.9 / 55.9; heads of 256 two of 4 50.0 against two of 5 52.4.  Many
-// rows take registers: one CTA of 7, with 32 rows an item where they fit (int8 at heads of 128 would spill: 24).
+// four of 3 12.6 / 56.7 / 57.5, two of 7 11.5 / 61.9 / 55.9; heads of 256 two of 4 50.0 against two of 5 52.4.  The
+// first is taken for all of them: a ninth less on the short call for 4 % more on many sequences.
+// Many rows take registers: one CTA of 7, with items of 32 rows; of 24 for int8 at heads of 128, where 32 spill a
+// little (128, 256, 512, 1024 rows over 8191 tokens: 24 an item 38.4, 59.4, 102, 185; 32 39.2, 60.4, 97, 177).
 template <int D, bool E4M3>
 cudaError_t plan_attends(eva_kv *h, int optin) {
     if constexpr (D <= 128) {
@@ -192,7 +194,8 @@ cudaError_t plan_attends(eva_kv *h, int optin) {
         if (e == cudaSuccess) e = plan_attend<D, 2, 5, 2, E4M3>(h, 1, optin);
         if (e == cudaSuccess) e = plan_attend<D, D < 128 || E4M3 ? 4 : 3, 7, 1, E4M3>(h, 2, optin);
         return e;
-    } else {                             // 16 rows a warp would not fit in its registers
+    } else {     // items of 8 rows for all: of 16 (one CTA of 7 warps) 34.2 against 29.4 us for three drafted tokens of
+                 // eight queries a key head, 39.3 / 36.9 for five, but 74 / 91 for 128 rows over 8191 tokens
         return plan_attend<D, 1, 4, 2, E4M3>(h, 0, optin);
     }
 }

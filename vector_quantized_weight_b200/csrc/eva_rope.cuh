@@ -157,8 +157,10 @@ struct RopeRaw {
 // W lanes a head (a power of two >= D/16).  Needs D a multiple of 16, R too in the
 // half layout, and every pointer and stride a multiple of 16 bytes.  A lane keeps the loads of its
 // next turns in flight (with one turn's, a prompt of 8192 tokens and 72 heads of
-// 128 took 86 us: 24 KB an SM are too few for the memory's latency; now 63 us, 4.8
-// TB/s, bound by instruction issue beside the memory).
+// 128 took 86 us: 24 KB an SM are too few for the memory's latency; now 62 us, 4.9
+// TB/s).  What it waits for now is shared memory: a turn reads its sines and weights
+// again, which keeps that path 74 % busy, with a third of the warps resident (80
+// registers); issue slots and DRAM are half busy.
 template <typename TI, typename TO, int W>
 __global__ void __launch_bounds__(kRopeThreads, 3) eva_rope_kernel(RopeParams p) {
     constexpr int kAhead = sizeof(TI) == 2 ? 2 : 1;
