@@ -476,7 +476,8 @@ typedef struct eva_kv *eva_kv_t;
 /*
  * A cache over caller-owned device buffers (16-byte aligned):
  *   k_pages, v_pages  codes [num_pages][kv_heads][page_size][head_dim], one byte each
- *   k_scale, v_scale  fp32 [num_pages][kv_heads], not negative
+ *   k_scale, v_scale  fp32 [num_pages][kv_heads], not negative, at most 1e30; to eva_kv_attend a value scale
+ *                     below 1e-30, 0 among them, is 1e-30
  * They keep their contents and must live as long as the handle.  The handle owns
  * the workspace of eva_kv_attend.  Waits for `stream`.
  */

@@ -269,6 +269,24 @@ def test_attend_counts_keys_of_zero_pages_beside_others():
     c.close()
 
 
+@pytest.mark.parametrize("low,high", [(1e-30, 1e-30), (1e30, 1e30), (1e-30, 1e-12), (1e12, 1e30)])
+def test_attend_with_value_scales_at_the_ends_of_their_range(low, high):
+    P, D, total = 16, 64, 900
+    r, pages = rng(151), -(-900 // 16)
+    k, v = (r.integers(-100, 101, (total, 1, D)).astype(float) for _ in range(2))
+    sk = np.full((pages, 1), 0.0078125)
+    sv = ref.f32(np.exp(np.log(low) + r.random((pages, 1)) * np.log(high / low)))
+    q = cuda(r.standard_normal((3, 2, D)), torch.float16)
+    c, table = one_sequence("int8", P, 2, k, v, sk, sv, out_dtype="float32")
+    lse = torch.empty((3, 2), device="cuda")
+    out = c.attend(q, i32([0, 3]), i32([total]), table, lse=lse)
+    assert c.status() == eva_vq.EVA_OK
+    want, wlse, bound = softmax_of(q.double().cpu().numpy(), k, v, sk, sv, P, D ** -0.5)
+    close(out, want, 1.02 * bound, torch.float32)      # an exponent near 110 is rounded by 2^-18, twice: each 1 % of 2^-11
+    np.testing.assert_allclose(lse.double().cpu().numpy(), wlse, atol=4e-5, rtol=2e-6)
+    c.close()
+
+
 @pytest.mark.parametrize("D,Hq,n,total", [(128, 8, 1, 300), (64, 4, 4, 90), (256, 4, 1, 200), (128, 8, 12, 900)])
 def test_attend_keeps_a_nan_in_its_row(D, Hq, n, total):
     c, table = make_cache("int8", [total], 64, 2, D, 111, Hq=Hq)
