@@ -229,6 +229,32 @@ def test_attend_joins_very_many_parts(cache, P, Hq, D, total, n):
     c.close()
 
 
+@pytest.mark.parametrize("cache,P,H,D,G,lens,n,softcap", [
+    ("e4m3", 32, 3, 256, 16, [1, 0, 0, 1491, 1, 900, 1, 1359, 1], [0, 0, 0, 1, 6, 4, 1, 1, 0], 30.0),
+    ("int8", 32, 3, 256, 8, [1491, 900, 1359], [1, 4, 1], 0.0), ("e4m3", 16, 2, 256, 2, [4000, 3100], [1, 1], 0.0),
+    ("int8", 64, 3, 128, 8, [3000, 1, 2500, 2700], [1, 6, 2, 1], 0.0), ("e4m3", 64, 3, 128, 8, [3000, 1, 2500], [1, 6, 2], 30.0),
+    ("int8", 32, 4, 64, 4, [5000, 4000], [1, 2], 0.0), ("e4m3", 32, 2, 64, 16, [4000, 3100], [5, 1], 0.0),
+    ("int8", 64, 2, 128, 8, [2500], [30], 0.0), ("e4m3", 64, 2, 128, 4, [2500], [40], 0.0),
+])
+def test_attend_repeats_itself_bit_for_bit(cache, P, H, D, G, lens, n, softcap):
+    """Many calls on one cache, all of it in the L2, so that copies come back fast: no stage is filled again before all of it
+    has been read."""
+    c, table = make_cache(cache, lens, P, H, D, 22294, Hq=H * G, softcap=softcap, out_dtype="float32")
+    starts = np.concatenate([[0], np.cumsum(n)])
+    rows = int(starts[-1])
+    q = cuda(rng(22294).standard_normal((rows, H * G, D)), torch.float16)
+    args = (i32(starts), i32(lens), i32(table))
+    outs = [c.attend(q, *args) for _ in range(200)]
+    assert c.status() == eva_vq.EVA_OK
+    with np.errstate(invalid="ignore"):
+        want, _, bound = ref.attend(q.double().cpu().numpy(), codes(c.k), c.k_scale.double().cpu().numpy(), codes(c.v),
+                                    c.v_scale.double().cpu().numpy(), starts, lens, table, softcap=softcap)
+    close(outs[0], want, bound, torch.float32)
+    for i, out in enumerate(outs):
+        assert torch.equal(out, outs[0]), i
+    c.close()
+
+
 def test_attend_sums_of_pages_of_zero_values():
     """2,200,000 keys whose values are all zero: zeros, and the logarithm of a sum that keeps within fp32."""
     P, D, total = 256, 64, 2200000

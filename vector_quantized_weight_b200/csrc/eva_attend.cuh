@@ -72,6 +72,7 @@ struct AttendParams {
     int window, out_f32, min_steps, wait_rounds;
     int inject;                        // test hook, 1: stream nothing, so that every wait runs out; 2: work on nothing
     float scale, cap;                  // cap 0: none
+    uint32_t nothing;                  // 0, but not to the compiler
 };
 
 struct alignas(64) AttendMaps {
@@ -850,12 +851,17 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 __syncwarp();
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");       // before the stage's next copy
             }
-            // O^T += V^T P^T; at 16 tokens a step one load brings two chunks of dimensions
+            // O^T += V^T P^T; at 16 tokens a step one load brings two chunks of dimensions.  `read` takes a register of each
+            // load: the stage is handed back when they are all there.  The order of the instructions alone does not do it:
+            // a copy into the stage overtook the last load of a step while the ring's first copies filled shared memory's
+            // bandwidth, and 32 dimensions got the values of another step.
+            uint32_t read = 0;
             if constexpr (MT > 1) {
 #pragma unroll
                 for (int ch = 0; ch < kChunks; ++ch) {
                     uint32_t r[4], a[2][4];
                     at_ldsm_t(addr(vt, lane, ch), r);
+                    read |= r[0];
                     AtCode<E4M3>::value(r[0], a[0][0], a[0][1]);
                     AtCode<E4M3>::value(r[1], a[0][2], a[0][3]);
                     AtCode<E4M3>::value(r[2], a[1][0], a[1][1]);
@@ -871,6 +877,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 for (int ch = 0; ch < kChunks; ch += 2) {
                     uint32_t r[4], a[2][4];
                     at_ldsm_t(addr(vt, lane & 15, ch + (lane >> 4)), r);
+                    read |= r[0];
                     AtCode<E4M3>::value(r[0], a[0][0], a[0][1]);
                     AtCode<E4M3>::value(r[1], a[0][2], a[0][3]);
                     AtCode<E4M3>::value(r[2], a[1][0], a[1][1]);
@@ -883,7 +890,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(free_a + 8 * st);
+            if (lane == 0) mbar_arrive(free_a + 8 * st + (read & p.nothing));
         }
         if (!ok) break;
         {
