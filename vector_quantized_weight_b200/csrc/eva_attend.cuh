@@ -853,8 +853,8 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
             }
             // O^T += V^T P^T; at 16 tokens a step one load brings two chunks of dimensions.  `read` takes a register of each
             // load: the stage is handed back when they are all there.  The order of the instructions alone does not do it:
-            // a copy into the stage overtook the last load of a step while the ring's first copies filled shared memory's
-            // bandwidth, and 32 dimensions got the values of another step.
+            // the next copy into a stage overtook the last load of a part's first step, and 32 dimensions got the values of
+            // another step (seen in repeated calls on a cache in the L2).
             uint32_t read = 0;
             if constexpr (MT > 1) {
 #pragma unroll
