@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");       // before the stage's next copy
             }
             // O^T += V^T P^T; at 16 tokens a step one load brings two chunks of dimensions.  `read` takes a register of each
-            // load: the stage is handed back when they are all there.  The order of the instructions alone does not do it:
+            // load: the stage is handed back when their data are there.  The order of the instructions alone does not do it:
             // the next copy into a stage overtook the last load of a part's first step, and 32 dimensions got the values of
             // another step (seen in repeated calls on a cache in the L2).
             uint32_t read = 0;
@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), CTAS)
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(free_a + 8 * st + (read & p.nothing));
+            if ((lane | (read & p.nothing)) == 0) mbar_arrive(free_a + 8 * st);
         }
         if (!ok) break;
         {
